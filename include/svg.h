@@ -326,6 +326,103 @@ svg_status svg_sparse_attn_noalloc(const void *qp, const void *kp, const void *v
 svg_status svg_unpermute(const void *xp, const int32_t *perm, int BH, int N, int D, void *x,
                          svg_stream_t stream);
 
+/* ------------------------------------------------------------------------ Q/K norm with rotation
+ * What a layer does between its projections and its attention, in one pass:
+ * the RMS norm of every head of Q and of K, the rotation by the token's
+ * position, and the move from token-major to head-major rows (V is moved too).
+ *
+ *     n = x * (mean over D of x^2 + eps)^(-1/2)      y = R(position) (w * n)
+ *
+ *   q          [B, N, Hq, D] bf16  view; element strides of B, N and H in the
+ *   k, v       [B, N, Hk, D] bf16  host arrays *_strides[3] (multiples of 8),
+ *                                  channels contiguous; k and v may be NULL
+ *   w_q, w_k   [D] fp32            weights; NULL: ones
+ *   cos, sin   [P, D/2] fp32       angles of every position; both NULL: no rotation
+ *   interleaved                    1: channels 2i, 2i+1 form pair i; 0: i, i + D/2
+ *   start      [B] int32           position of a sequence's token 0 (NULL: 0)
+ *   q_out      [B*Hq, N, D]   bf16 row n
+ *   k_out, v_out [B*Hk, cap, D] bf16 row start[b] + n: buffers of cap rows per
+ *                                  head, a K/V cache; other rows stay as they are
+ * A token with a negative position is padding: its row of q_out becomes zero,
+ * nothing is stored for k and v.  A position at or beyond P or cap is treated
+ * the same way and recorded as SVG_ERR_DEVICE_CHECK (without start: P and cap
+ * are checked on the host).  Norms are formed in fp32, outputs rounded once.
+ */
+svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                            const void *v, const int64_t *v_strides, const float *w_q, const float *w_k,
+                            const float *cos, const float *sin, int P, int B, int N, int Hq, int Hk, int D,
+                            float eps, int interleaved, const int32_t *start, void *q_out, void *k_out, void *v_out,
+                            int cap, svg_stream_t stream);
+
+/* Its gradient.  dq_out, dk_out and dv_out are laid out like the outputs, dq,
+ * dk and dv like the inputs (strided views); dw_q, dw_k [D] fp32 (NULL to
+ * skip) are sums over all rows, in a fixed order.  Padding rows get zeros. */
+size_t svg_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, int D);
+svg_status svg_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *dv_out, const void *q,
+                                     const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                                     const float *w_q, const float *w_k, const float *cos, const float *sin, int P,
+                                     int B, int N, int Hq, int Hk, int D, float eps, int interleaved,
+                                     const int32_t *start, int cap, void *dq, const int64_t *dq_strides, void *dk,
+                                     const int64_t *dk_strides, void *dv, const int64_t *dv_strides, float *dw_q,
+                                     float *dw_k, void *ws, size_t ws_bytes, svg_stream_t stream);
+
+/* ------------------------------------------------------------------------ blocks chosen for each query
+ * Attention in which every query has its own list of key blocks, with query
+ * heads that share key heads (query head h reads key head h / (BHq/BHk), at
+ * most 16 to one), and a context that grows (a K/V cache):
+ *
+ *   svg_block_mean          mean key of every block
+ *   svg_block_select        per query: forced blocks and those of the largest
+ *                           (sum of the group's q) . mean
+ *   svg_block_attn          softmax attention over the listed blocks
+ *   svg_block_attn_backward its gradient (lists are constants)
+ *
+ * Shared arguments: B sequences; k, v [BHk, Nk, D] bf16 with kv_len[b] keys in
+ * use (int32 [B], held to 0..Nk; NULL: Nk), block = 64 or 128 keys, block j =
+ * rows [j*block, (j+1)*block); nblk = ceil(Nk/block) <= 4096.  The Nq queries
+ * are the last tokens of their sequence: query n has position
+ * kv_len[b] - Nq + n and with causal = 1 sees the keys up to it (none when
+ * that is negative: left padding), with causal = 0 all keys in use.
+ * Lists sel [BHk, Nq, topk] int32, topk <= 1024.  Workspaces as elsewhere; a
+ * call whose *_workspace_size() is 0 takes ws = NULL.
+ */
+
+/* mean [BHk, nblk, D] fp32: mean over the block's keys in use (fp64 sum,
+ * rounded once; a block without keys: zeros).  fresh > 0: only the blocks that
+ * hold any of the sequence's last `fresh` keys are formed, others stay. */
+svg_status svg_block_mean(const void *k, int BHk, int B, int Nk, int D, int block, const int32_t *kv_len, int fresh,
+                          float *mean, svg_stream_t stream);
+
+/* sel: block ids in ascending order, filled up with -1.  Of the blocks that
+ * hold a visible key, the first `sink` and the `local` ones up to the query's
+ * own are taken, the rest by score (NaN counts as -inf), the lower block on a
+ * tie, until topk are listed.  The choice is the one of exact (fp64) scores.
+ * Requires sink + local <= topk, and local >= 1 when causal. */
+size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int block);
+svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, int B, int Nq, int Nk, int D,
+                            int block, int topk, int sink, int local, int causal, const int32_t *kv_len,
+                            int32_t *sel, void *ws, size_t ws_bytes, svg_stream_t stream);
+
+/* o [BHq, Nq, D] bf16, lse [BHq, Nq] fp32 (natural log, NULL to skip).  Lists
+ * may be in any order; ids outside [0, nblk) are passed over and an id given
+ * twice counts once.  A query without a visible key gets zeros and lse = -inf.
+ * scale <= 0 selects 1/sqrt(D).  Blocks that a query does not list and rows
+ * beyond kv_len do not reach it, whatever they hold. */
+size_t svg_block_attn_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block);
+svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, int BHk, int B, int Nq, int Nk, int D,
+                          const int32_t *sel, int topk, int block, int causal, float scale, const int32_t *kv_len,
+                          void *o, float *lse, void *ws, size_t ws_bytes, svg_stream_t stream);
+
+/* dq [BHq, Nq, D], dk, dv [BHk, Nk, D] bf16 from dout, the forward call's
+ * inputs and its o and lse.  Every element is written (zeros where nothing
+ * was listed); sums run in a fixed order. */
+size_t svg_block_attn_backward_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block);
+svg_status svg_block_attn_backward(const void *dout, const void *q, const void *k, const void *v, const void *o,
+                                   const float *lse, int BHq, int BHk, int B, int Nq, int Nk, int D,
+                                   const int32_t *sel, int topk, int block, int causal, float scale,
+                                   const int32_t *kv_len, void *dq, void *dk, void *dv, void *ws, size_t ws_bytes,
+                                   svg_stream_t stream);
+
 /* ------------------------------------------------------------------------ errors and limits
  * svg_get_error synchronises `stream`, then returns and clears the device
  * error word of the current device (SVG_OK when nothing was recorded;
@@ -349,7 +446,8 @@ typedef enum svg_error_site {
   SVG_SITE_KMEANS_MMA = 7,      /* k-means assign: MMA issuer warp */
   SVG_SITE_KMEANS_EPI = 8,      /* k-means assign: epilogue warps */
   SVG_SITE_KMEANS_RANGE = 9,    /* k-means update: cluster id outside [0, C) */
-  SVG_SITE_KMEANS_DRAIN = 10    /* k-means assign: waiting for copies in flight after an abort */
+  SVG_SITE_KMEANS_DRAIN = 10,   /* k-means assign: waiting for copies in flight after an abort */
+  SVG_SITE_ROPE_RANGE = 11      /* Q/K norm with rotation: position beyond the table or the buffer */
 } svg_error_site;
 
 /* Same as svg_get_error (synchronises, returns and clears the error word),

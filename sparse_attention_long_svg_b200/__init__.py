@@ -11,6 +11,11 @@ Stages (Sparse VideoGen2, section 2): ``kmeans`` -> ``permute`` ->
 the whole layer.  Options: ``sparse_attn_gather`` (K/V rows fetched through
 the K permutation), ``dynrad_select`` (DynamicRad block masks),
 ``quantize_e4m3`` + ``sparse_attn_fp8`` (Q K^T on 8-bit tensor cores).
+
+Around it (blocks.py): ``qk_norm_rope`` prepares a projection's Q, K and V for
+any of the attention calls or appends them to a K/V cache; ``block_mean`` ->
+``block_select`` -> ``block_attn`` (``block_attention`` runs all three) is
+attention over key blocks chosen for each query; both have gradients.
 """
 from __future__ import annotations
 
@@ -64,6 +69,16 @@ SIGNATURES = {
     "svg_profile_read": (_I, [_I, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int),
                               ctypes.POINTER(ctypes.c_int)]),
     "svg_profile_attn_pairs": (_I, [ctypes.POINTER(ctypes.c_uint64)]),
+    "svg_qk_norm_rope": (_I, [_P] * 10 + [_I] * 6 + [_F, _I] + [_P] * 4 + [_I, _P]),
+    "svg_qk_norm_rope_backward_workspace_size": (_SZ, [_I] * 5),
+    "svg_qk_norm_rope_backward": (_I, [_P] * 11 + [_I] * 6 + [_F, _I, _P, _I] + [_P] * 9 + [_SZ, _P]),
+    "svg_block_mean": (_I, [_P, _I, _I, _I, _I, _I, _P, _I, _P, _P]),
+    "svg_block_select_workspace_size": (_SZ, [_I] * 4),
+    "svg_block_select": (_I, [_P, _P] + [_I] * 11 + [_P, _P, _P, _SZ, _P]),
+    "svg_block_attn_workspace_size": (_SZ, [_I] * 7),
+    "svg_block_attn": (_I, [_P] * 3 + [_I] * 6 + [_P, _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]),
+    "svg_block_attn_backward_workspace_size": (_SZ, [_I] * 7),
+    "svg_block_attn_backward": (_I, [_P] * 6 + [_I] * 6 + [_P, _I, _I, _I, _F, _P, _P, _P, _P, _P, _SZ, _P]),
 }
 
 PROFILE_KERNELS = {"kmeans_assign": 0, "sparse_attn": 1}
@@ -136,7 +151,7 @@ def get_error(stream=None) -> int:
 
 ERROR_SITES = {0: "none", 1: "attention producer", 2: "attention MMA issuer", 3: "attention softmax",
                4: "attention drain", 5: "attention planning", 6: "permute range", 7: "k-means MMA issuer",
-               8: "k-means epilogue", 9: "k-means range", 10: "k-means drain"}
+               8: "k-means epilogue", 9: "k-means range", 10: "k-means drain", 11: "rotation range"}
 
 
 def get_error_detail(stream=None) -> Tuple[int, str, int]:
@@ -623,3 +638,7 @@ def svg_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, mu_q: torch
 
 def default_scale(D: int) -> float:
     return 1.0 / math.sqrt(D)
+
+
+from .blocks import (block_attention, block_attn, block_attn_backward, block_mean, block_select,  # noqa: E402,F401
+                     qk_norm_rope, qk_norm_rope_backward, rope_table)

@@ -1,0 +1,820 @@
+// Softmax attention of every query over the keys of its own list of key
+// blocks (svg_block_attn) and its gradient (svg_block_attn_backward).
+//
+// The G = Hq/Hk query heads of a key head share the query's list, so the heads
+// of floor(16/G) neighbouring tokens form the 16 rows of a warp's matrix tile.
+// A CTA marks its tokens' blocks in shared bit sets, walks over their union in
+// ascending order, 64 keys at a time, and each row takes part in the blocks
+// that its own token lists: others leave its maximum, sum and accumulator as
+// they were (also where such a block holds infinities or NaN).
+//
+//   S = scale Q K^T over the visible keys;  m, l: running maximum and sum
+//   O = sum exp(S - m) V / l;  lse = m + log l;  no visible key: O = 0, lse = -inf
+// gradient, with P = exp(S - lse), delta = rowsum(dO O):
+//   dS = P (dO V^T - delta);  dQ = scale dS K;  dK = scale dS^T Q;  dV = P^T dO
+#pragma once
+
+#include "blocksel.cuh"
+#include "common.cuh"
+#include "mma.cuh"
+
+namespace svg {
+
+constexpr int kBaTile = 64;            // keys per step
+constexpr int kBaThreads = 128;
+constexpr int kBaMaxGroup = 16;
+constexpr int kBaMaxSplits = 64;
+
+struct BlockAttnArgs {
+  const __nv_bfloat16 *q, *k, *v;      // [BHk*G, Nq, D], [BHk, Nk, D]
+  const int32_t *sel, *kv_len;         // [BHk, Nq, topk], [B] or nullptr
+  __nv_bfloat16 *o;
+  float *lse;                          // [BHk*G, Nq], may be nullptr
+  float *part_o, *part_lse;            // splits: [splits][BHk*G*Nq][D], [splits][BHk*G*Nq] (log2 units)
+  // backward
+  const __nv_bfloat16 *dout, *out;
+  const float *lse_in;
+  float *delta;
+  __nv_bfloat16 *dq, *dk, *dv;
+  uint32_t *rev;                       // [BHk][nblk][ceil(Nq/32)] bit sets: who lists the block
+  int32_t *item_first;                 // [BHk * key tiles + 1] first work item of a key tile
+  int32_t *slot_first;                 // [BHk * key tiles] first slot of a tile with several items
+  int32_t *items;                      // key tile of every work item
+  float *part_kv;                      // [slot][2][64][D]
+  int BHk, G, heads_per_seq, Nq, Nk, nblk, block, topk, causal, splits;
+  int item_tokens;
+  float scale, scale_log2;
+};
+
+// Keys the query n sees.
+__device__ __forceinline__ int query_seen(const BlockAttnArgs &a, int len, int n) {
+  return a.causal ? min(len - a.Nq + n + 1, len) : len;
+}
+
+// Bit sets of the blocks of `tokens` tokens from n0 on (one per token, W words
+// each, at `bits`), their union as an ascending list; returns its length.  Ids
+// outside the sequence and blocks without a visible key are passed over.
+__device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int len, int n0, int tokens, int W,
+                                           uint32_t *bits, uint16_t *list, int *count) {
+  for (int i = threadIdx.x; i < tokens * W; i += kBaThreads) bits[i] = 0;
+  __syncthreads();
+  const int32_t *sel = a.sel + (static_cast<int64_t>(head) * a.Nq + n0) * a.topk;
+  for (int i = threadIdx.x; i < tokens * a.topk; i += kBaThreads) {
+    const int tok = i / a.topk;
+    if (n0 + tok >= a.Nq) break;
+    const int j = sel[i];
+    if (j >= 0 && j < a.nblk && static_cast<int64_t>(j) * a.block < query_seen(a, len, n0 + tok))
+      atomicOr(&bits[tok * W + (j >> 5)], 1u << (j & 31));
+  }
+  __syncthreads();
+  if (warp_id() == 0) {
+    int at = 0;
+    for (int w0 = 0; w0 < W; w0 += 32) {
+      const int w = w0 + lane_id();
+      uint32_t u = 0;
+      if (w < W)
+        for (int t = 0; t < tokens; ++t) u |= bits[t * W + w];
+      int pre = __popc(u);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, pre, o);
+        if (static_cast<int>(lane_id()) >= o) pre += x;
+      }
+      const int all = __shfl_sync(0xffffffffu, pre, 31);
+      int p = at + pre - __popc(u);
+      while (u) {
+        list[p++] = static_cast<uint16_t>(w * 32 + __ffs(u) - 1);
+        u &= u - 1;
+      }
+      at += all;
+    }
+    if (lane_id() == 0) *count = at;
+  }
+  __syncthreads();
+  return *count;
+}
+
+// Rows [key0, key0 + 64) of a [Nk, D] matrix to a shared tile by `threads`
+// threads; rows from `len` on become zeros.
+template <int D>
+__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *src, int key0, int len, int tid,
+                                          int threads) {
+  constexpr int COLS = D / 8;
+  for (int i = tid; i < kBaTile * COLS; i += threads) {
+    const int r = i / COLS, c = i % COLS;
+    const bool in = key0 + r < len;
+    cp_async16(dst + tile_at<D>(r, c), src + (in ? static_cast<int64_t>(key0 + r) * D + 8 * c : 0), in ? 16u : 0u);
+  }
+}
+
+// A operand (16 rows x D channels) straight from global memory.
+template <int D>
+__device__ __forceinline__ void load_rows(uint32_t (&f)[D / 16][4], const __nv_bfloat16 *r0, const __nv_bfloat16 *r1) {
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) {
+    const int c = 16 * ks + frag_col();
+    f[ks][0] = r0 ? *reinterpret_cast<const uint32_t *>(r0 + c) : 0u;
+    f[ks][1] = r1 ? *reinterpret_cast<const uint32_t *>(r1 + c) : 0u;
+    f[ks][2] = r0 ? *reinterpret_cast<const uint32_t *>(r0 + c + 8) : 0u;
+    f[ks][3] = r1 ? *reinterpret_cast<const uint32_t *>(r1 + c + 8) : 0u;
+  }
+}
+
+// One row of a 16-row tile as this thread sees it.
+struct BaRow {
+  int64_t row;      // row of [BHk*G*Nq], -1: none
+  int tok;          // token within the CTA's
+  int seen;         // keys it sees
+};
+__device__ __forceinline__ BaRow ba_row(const BlockAttnArgs &a, int head, int len, int n0, int tok0, int r) {
+  BaRow x;
+  const int per = 16 / a.G;
+  x.tok = tok0 + r / a.G;
+  const int n = n0 + x.tok;
+  const bool in = r < per * a.G && n < a.Nq;
+  x.row = in ? (static_cast<int64_t>(head) * a.G + r % a.G) * a.Nq + n : -1;
+  x.seen = in ? query_seen(a, len, n) : 0;
+  if (!in) x.tok = tok0;
+  return x;
+}
+
+// Shared memory: tiles, then bit sets, block list, its length.
+template <int D>
+__host__ __device__ inline size_t block_attn_smem(int tiles, int tokens, int nblk) {
+  const size_t W = (nblk + 31) / 32;
+  return static_cast<size_t>(tiles) * kBaTile * D * 2 + static_cast<size_t>(tokens) * W * 4 +
+         (static_cast<size_t>(nblk) * 2 + 15) / 16 * 16 + 16;
+}
+
+// FEW = false: 4 warps x 16 rows share each K/V tile (two tiles in flight).
+// FEW = true (at most floor(16/G) queries): all warps hold the same 16 rows and
+// take every fourth tile, each through its own buffer; the CTA joins them.
+// gridDim.y splits the union's tiles; a second kernel joins the splits.
+template <int D, bool FEW>
+__global__ void __launch_bounds__(kBaThreads) block_attn_kernel(const BlockAttnArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int TILE = kBaTile * D * 2, NT = D / 8;
+  constexpr int TILES = FEW ? 8 : 4;
+  const int per = 16 / a.G;                       // tokens of a warp
+  const int tokens = FEW ? per : 4 * per;
+  const int ntiles = (a.Nq + tokens - 1) / tokens;
+  const int head = blockIdx.x % a.BHk;
+  const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;   // long causal rows first
+  const int W = (a.nblk + 31) / 32;
+  const int warp = warp_id();
+  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + TILES * TILE);
+  uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
+  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(TILES, tokens, a.nblk) - 16);
+  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
+  const int sub = a.block / kBaTile;
+  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
+  const int each = (total + a.splits - 1) / a.splits;
+  const int u0 = min(static_cast<int>(blockIdx.y) * each, total), u1 = min(u0 + each, total);
+
+  const int tok0 = FEW ? 0 : warp * per;
+  const BaRow x0 = ba_row(a, head, len, n0, tok0, frag_row());
+  const BaRow x1 = ba_row(a, head, len, n0, tok0, frag_row() + 8);
+  uint32_t qf[D / 16][4];
+  load_rows<D>(qf, x0.row >= 0 ? a.q + x0.row * D : nullptr, x1.row >= 0 ? a.q + x1.row * D : nullptr);
+  const __nv_bfloat16 *kh = a.k + static_cast<int64_t>(head) * a.Nk * D;
+  const __nv_bfloat16 *vh = a.v + static_cast<int64_t>(head) * a.Nk * D;
+
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+  const uint32_t base = smem_u32(smem);
+  const int first = FEW ? u0 + warp : u0, step = FEW ? 4 : 1;
+  const int tid = FEW ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
+  const int nthr = FEW ? 32 : kBaThreads;
+  auto buffer = [&](int i) { return base + static_cast<uint32_t>(FEW ? warp : (i & 1)) * 2 * TILE; };
+  auto key_of = [&](int u) { return static_cast<int>(list[u / sub]) * a.block + (u % sub) * kBaTile; };
+  auto fetch = [&](int i) {
+    const int u = first + i * step;
+    if (u < u1) {
+      const int key0 = key_of(u);
+      load_tile<D>(buffer(i), kh, key0, len, tid, nthr);
+      load_tile<D>(buffer(i) + TILE, vh, key0, len, tid, nthr);
+    }
+    cp_async_commit();
+  };
+  fetch(0);
+  for (int i = 0; first + i * step < u1; ++i) {
+    if (FEW) {
+      cp_async_wait<0>();
+      __syncwarp();
+    } else {
+      fetch(i + 1);
+      cp_async_wait<1>();
+      __syncthreads();
+    }
+    const int u = first + i * step;
+    const int blk = list[u / sub], key0 = key_of(u);
+    const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
+    const bool on1 = x1.row >= 0 && ((bits[x1.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x1.seen;
+    if (__any_sync(0xffffffffu, on0 || on1)) {
+      const uint32_t kt = buffer(i), vt = kt + TILE;
+      float s[8][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+        for (int t = 0; t < 8; t += 2) {
+          uint32_t b[4];
+          ldsm_x4(ldsm_b<D>(kt, 8 * t, ks), b);
+          mma_bf16(s[t], qf[ks], b[0], b[1]);
+          mma_bf16(s[t + 1], qf[ks], b[2], b[3]);
+        }
+      const int end0 = on0 ? x0.seen - key0 : 0, end1 = on1 ? x1.seen - key0 : 0;
+      float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int c = 8 * t + frag_col();
+        s[t][0] = c < end0 ? s[t][0] * a.scale_log2 : -INFINITY;
+        s[t][1] = c + 1 < end0 ? s[t][1] * a.scale_log2 : -INFINITY;
+        s[t][2] = c < end1 ? s[t][2] * a.scale_log2 : -INFINITY;
+        s[t][3] = c + 1 < end1 ? s[t][3] * a.scale_log2 : -INFINITY;
+        t0 = fmaxf(t0, fmaxf(s[t][0], s[t][1]));
+        t1 = fmaxf(t1, fmaxf(s[t][2], s[t][3]));
+      }
+      const float n0m = fmaxf(m0, quad_max(t0)), n1m = fmaxf(m1, quad_max(t1));
+      const float b0 = n0m == -INFINITY ? 0.f : n0m, b1 = n1m == -INFINITY ? 0.f : n1m;
+      const float f0 = on0 ? ex2_approx(m0 - b0) : 1.f, f1 = on1 ? ex2_approx(m1 - b1) : 1.f;
+      m0 = n0m;
+      m1 = n1m;
+      l0 *= f0;
+      l1 *= f1;
+      uint32_t p[4][4];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const float p0 = ex2_approx(s[t][0] - b0), p1 = ex2_approx(s[t][1] - b0);
+        const float p2 = ex2_approx(s[t][2] - b1), p3 = ex2_approx(s[t][3] - b1);
+        l0 += p0 + p1;
+        l1 += p2 + p3;
+        // P as bf16 for the matrix product: 2^-8 relative to each weight; the sum keeps fp32
+        p[t / 2][(t & 1) * 2] = pack_bf16(p0, p1);
+        p[t / 2][(t & 1) * 2 + 1] = pack_bf16(p2, p3);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        float c0[4] = {acc[t][0] * f0, acc[t][1] * f0, acc[t][2] * f1, acc[t][3] * f1};
+        float c1[4] = {acc[t + 1][0] * f0, acc[t + 1][1] * f0, acc[t + 1][2] * f1, acc[t + 1][3] * f1};
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          uint32_t b[4];
+          ldsm_x4_trans(ldsm_a<D>(vt, 16 * ks, t / 2), b);
+          mma_bf16(c0, p[ks], b[0], b[1]);
+          mma_bf16(c1, p[ks], b[2], b[3]);
+        }
+        // a row that does not list this block keeps its accumulator, whatever V holds
+        acc[t][0] = on0 ? c0[0] : acc[t][0];
+        acc[t][1] = on0 ? c0[1] : acc[t][1];
+        acc[t][2] = on1 ? c0[2] : acc[t][2];
+        acc[t][3] = on1 ? c0[3] : acc[t][3];
+        acc[t + 1][0] = on0 ? c1[0] : acc[t + 1][0];
+        acc[t + 1][1] = on0 ? c1[1] : acc[t + 1][1];
+        acc[t + 1][2] = on1 ? c1[2] : acc[t + 1][2];
+        acc[t + 1][3] = on1 ? c1[3] : acc[t + 1][3];
+      }
+    }
+    if (FEW) {
+      __syncwarp();
+      fetch(i + 1);
+    } else {
+      __syncthreads();
+    }
+  }
+  cp_async_wait<0>();
+  l0 = quad_sum(l0);
+  l1 = quad_sum(l1);
+
+  if (FEW) {
+    // join the four warps' sums: [warp][16 rows][D] and maxima / sums behind
+    __syncthreads();
+    float *so = reinterpret_cast<float *>(smem);
+    float *sm = so + 4 * 16 * D, *sl = sm + 64;
+    const int r0 = frag_row();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int c = 8 * t + frag_col();
+      *reinterpret_cast<float2 *>(so + (warp * 16 + r0) * D + c) = make_float2(acc[t][0], acc[t][1]);
+      *reinterpret_cast<float2 *>(so + (warp * 16 + r0 + 8) * D + c) = make_float2(acc[t][2], acc[t][3]);
+    }
+    if ((lane_id() & 3) == 0) {
+      sm[warp * 16 + r0] = m0;
+      sm[warp * 16 + r0 + 8] = m1;
+      sl[warp * 16 + r0] = l0;
+      sl[warp * 16 + r0 + 8] = l1;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * D / 2; i += kBaThreads) {
+      const int r = i / (D / 2), c = (i % (D / 2)) * 2;
+      const BaRow x = ba_row(a, head, len, n0, 0, r);
+      if (x.row < 0) continue;
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, sm[w * 16 + r]);
+      const float b = m == -INFINITY ? 0.f : m;
+      float l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = ex2_approx(sm[w * 16 + r] - b);
+        const float2 v = *reinterpret_cast<const float2 *>(so + (w * 16 + r) * D + c);
+        l += f * sl[w * 16 + r];
+        // a warp without a visible key holds zeros
+        y0 += f * v.x;
+        y1 += f * v.y;
+      }
+      const bool none = m == -INFINITY && l == 0.f;
+      const float inv = none ? 0.f : 1.f / l;
+      y0 *= inv;
+      y1 *= inv;
+      const float lse2 = none ? -INFINITY : m + log2f(l);
+      if (a.splits > 1) {
+        const int64_t pr = static_cast<int64_t>(blockIdx.y) * a.BHk * a.G * a.Nq + x.row;
+        *reinterpret_cast<float2 *>(a.part_o + pr * D + c) = make_float2(y0, y1);
+        if (c == 0) a.part_lse[pr] = lse2;
+      } else {
+        *reinterpret_cast<uint32_t *>(a.o + x.row * D + c) = pack_bf16(y0, y1);
+        if (c == 0 && a.lse) a.lse[x.row] = lse2 * 0.69314718055994531f;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const BaRow &x = half ? x1 : x0;
+    const float m = half ? m1 : m0, l = half ? l1 : l0;
+    if (x.row < 0) continue;
+    const bool none = m == -INFINITY && l == 0.f;
+    const float inv = none ? 0.f : 1.f / l;
+    const float lse2 = none ? -INFINITY : m + log2f(l);
+    const bool split = a.splits > 1;
+    const int64_t pr = static_cast<int64_t>(blockIdx.y) * a.BHk * a.G * a.Nq + x.row;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float y0 = acc[t][2 * half] * inv, y1 = acc[t][2 * half + 1] * inv;
+      const int c = 8 * t + frag_col();
+      if (split)
+        *reinterpret_cast<float2 *>(a.part_o + pr * D + c) = make_float2(y0, y1);
+      else
+        *reinterpret_cast<uint32_t *>(a.o + x.row * D + c) = pack_bf16(y0, y1);
+    }
+    if ((lane_id() & 3) == 0) {
+      if (split)
+        a.part_lse[pr] = lse2;
+      else if (a.lse)
+        a.lse[x.row] = lse2 * 0.69314718055994531f;
+    }
+  }
+}
+
+// Joins the splits of a row: one warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) block_attn_join_kernel(const BlockAttnArgs a) {
+  constexpr int E = D / 32;
+  const int64_t rows = static_cast<int64_t>(a.BHk) * a.G * a.Nq;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + warp_id();
+  if (row >= rows) return;
+  float m = -INFINITY;
+  for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_lse[s * rows + row]);
+  const float b = m == -INFINITY ? 0.f : m;
+  float l = 0.f, y[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = 0.f;
+  for (int s = 0; s < a.splits; ++s) {
+    const float z = a.part_lse[s * rows + row];
+    const float f = z == -INFINITY ? 0.f : ex2_approx(z - b);
+    l += f;
+    const float *src = a.part_o + (s * rows + row) * D + lane_id() * E;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(src + e);
+      y[e] += f * v.x;
+      y[e + 1] += f * v.y;
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    *reinterpret_cast<uint32_t *>(a.o + row * D + lane_id() * E + e) = pack_bf16(y[e] * inv, y[e + 1] * inv);
+  if (a.lse && lane_id() == 0) a.lse[row] = (l == 0.f ? -INFINITY : b + log2f(l)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------ gradient
+// dQ (and delta for the second kernel): the forward kernel's walk with two more
+// products per tile, 32 keys at a time to stay in registers.
+template <int D>
+__global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAttnArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int TILE = kBaTile * D * 2, NT = D / 8;
+  const int per = 16 / a.G, tokens = 4 * per;
+  const int ntiles = (a.Nq + tokens - 1) / tokens;
+  const int head = blockIdx.x % a.BHk;
+  const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;
+  const int W = (a.nblk + 31) / 32;
+  const int warp = warp_id();
+  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + 4 * TILE);
+  uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
+  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(4, tokens, a.nblk) - 16);
+  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
+  const int sub = a.block / kBaTile;
+  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
+
+  const BaRow x0 = ba_row(a, head, len, n0, warp * per, frag_row());
+  const BaRow x1 = ba_row(a, head, len, n0, warp * per, frag_row() + 8);
+  uint32_t qf[D / 16][4], df[D / 16][4];
+  load_rows<D>(qf, x0.row >= 0 ? a.out + x0.row * D : nullptr, x1.row >= 0 ? a.out + x1.row * D : nullptr);
+  load_rows<D>(df, x0.row >= 0 ? a.dout + x0.row * D : nullptr, x1.row >= 0 ? a.dout + x1.row * D : nullptr);
+  float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float p = __uint_as_float(qf[ks][e] << 16) * __uint_as_float(df[ks][e] << 16) +
+                      __uint_as_float(qf[ks][e] & 0xFFFF0000u) * __uint_as_float(df[ks][e] & 0xFFFF0000u);
+      if (e & 1) d1 += p;
+      else d0 += p;
+    }
+  d0 = quad_sum(d0);
+  d1 = quad_sum(d1);
+  if ((lane_id() & 3) == 0) {
+    if (x0.row >= 0) a.delta[x0.row] = d0;
+    if (x1.row >= 0) a.delta[x1.row] = d1;
+  }
+  load_rows<D>(qf, x0.row >= 0 ? a.q + x0.row * D : nullptr, x1.row >= 0 ? a.q + x1.row * D : nullptr);
+  const float z0 = x0.row >= 0 ? a.lse_in[x0.row] * 1.4426950408889634f : 0.f;
+  const float z1 = x1.row >= 0 ? a.lse_in[x1.row] * 1.4426950408889634f : 0.f;
+  const __nv_bfloat16 *kh = a.k + static_cast<int64_t>(head) * a.Nk * D;
+  const __nv_bfloat16 *vh = a.v + static_cast<int64_t>(head) * a.Nk * D;
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+  const uint32_t base = smem_u32(smem);
+  auto key_of = [&](int u) { return static_cast<int>(list[u / sub]) * a.block + (u % sub) * kBaTile; };
+  auto fetch = [&](int u) {
+    if (u < total) {
+      const uint32_t buf = base + static_cast<uint32_t>(u & 1) * 2 * TILE;
+      load_tile<D>(buf, kh, key_of(u), len, threadIdx.x, kBaThreads);
+      load_tile<D>(buf + TILE, vh, key_of(u), len, threadIdx.x, kBaThreads);
+    }
+    cp_async_commit();
+  };
+  fetch(0);
+  for (int u = 0; u < total; ++u) {
+    fetch(u + 1);
+    cp_async_wait<1>();
+    __syncthreads();
+    const int blk = list[u / sub], key0 = key_of(u);
+    const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
+    const bool on1 = x1.row >= 0 && ((bits[x1.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x1.seen;
+    if (__any_sync(0xffffffffu, on0 || on1)) {
+      const uint32_t kt = base + static_cast<uint32_t>(u & 1) * 2 * TILE, vt = kt + TILE;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float s[4][4], dp[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[t][e] = dp[t][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+#pragma unroll
+          for (int t = 0; t < 4; t += 2) {
+            uint32_t b[4];
+            ldsm_x4(ldsm_b<D>(kt, 32 * h + 8 * t, ks), b);
+            mma_bf16(s[t], qf[ks], b[0], b[1]);
+            mma_bf16(s[t + 1], qf[ks], b[2], b[3]);
+            ldsm_x4(ldsm_b<D>(vt, 32 * h + 8 * t, ks), b);
+            mma_bf16(dp[t], df[ks], b[0], b[1]);
+            mma_bf16(dp[t + 1], df[ks], b[2], b[3]);
+          }
+        const int end0 = on0 ? x0.seen - key0 : 0, end1 = on1 ? x1.seen - key0 : 0;
+        uint32_t ds[2][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int c = 32 * h + 8 * t + frag_col();
+          float g[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool in = c + (e & 1) < (e < 2 ? end0 : end1);
+            const float pr = ex2_approx(s[t][e] * a.scale_log2 - (e < 2 ? z0 : z1));
+            g[e] = in ? pr * (dp[t][e] - (e < 2 ? d0 : d1)) : 0.f;
+          }
+          ds[t / 2][(t & 1) * 2] = pack_bf16(g[0], g[1]);
+          ds[t / 2][(t & 1) * 2 + 1] = pack_bf16(g[2], g[3]);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; t += 2) {
+          float c0[4] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
+          float c1[4] = {acc[t + 1][0], acc[t + 1][1], acc[t + 1][2], acc[t + 1][3]};
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            uint32_t b[4];
+            ldsm_x4_trans(ldsm_a<D>(kt, 32 * h + 16 * ks, t / 2), b);
+            mma_bf16(c0, ds[ks], b[0], b[1]);
+            mma_bf16(c1, ds[ks], b[2], b[3]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool on = e < 2 ? on0 : on1;
+            acc[t][e] = on ? c0[e] : acc[t][e];
+            acc[t + 1][e] = on ? c1[e] : acc[t + 1][e];
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int c = 8 * t + frag_col();
+    if (x0.row >= 0)
+      *reinterpret_cast<uint32_t *>(a.dq + x0.row * D + c) = pack_bf16(acc[t][0] * a.scale, acc[t][1] * a.scale);
+    if (x1.row >= 0)
+      *reinterpret_cast<uint32_t *>(a.dq + x1.row * D + c) = pack_bf16(acc[t][2] * a.scale, acc[t][3] * a.scale);
+  }
+}
+
+// Who lists a block: bit sets over the queries (order of the atomics is of no
+// account).
+__global__ void __launch_bounds__(256) block_attn_reverse_kernel(const BlockAttnArgs a) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= static_cast<int64_t>(a.BHk) * a.Nq * a.topk) return;
+  const int64_t q = i / a.topk;
+  const int head = static_cast<int>(q / a.Nq), n = static_cast<int>(q % a.Nq);
+  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
+  const int j = a.sel[i];
+  if (j < 0 || j >= a.nblk || static_cast<int64_t>(j) * a.block >= query_seen(a, len, n)) return;
+  const int64_t WQ = (a.Nq + 31) / 32;
+  atomicOr(a.rev + (static_cast<int64_t>(head) * a.nblk + j) * WQ + (n >> 5), 1u << (n & 31));
+}
+
+// Work items of every key tile: ceil(queries / item_tokens), at least one.  One
+// warp counts a block's queries.
+__global__ void __launch_bounds__(256) block_attn_count_kernel(const BlockAttnArgs a) {
+  const int sub = a.block / kBaTile;
+  const int64_t blk = static_cast<int64_t>(blockIdx.x) * 8 + warp_id();
+  if (blk >= static_cast<int64_t>(a.BHk) * a.nblk) return;
+  const int WQ = (a.Nq + 31) / 32;
+  int c = 0;
+  for (int w = lane_id(); w < WQ; w += 32) c += __popc(a.rev[blk * WQ + w]);
+  c = __reduce_add_sync(0xffffffffu, c);
+  if (static_cast<int>(lane_id()) < sub)
+    a.item_first[blk * sub + lane_id()] = max(1, (c + a.item_tokens - 1) / a.item_tokens);
+}
+
+// Exclusive sums over the key tiles: items (in place) and slots (of tiles with
+// several items), as the high and low half of one 64-bit sum; and the tile of
+// every item.
+__global__ void __launch_bounds__(1024) block_attn_items_kernel(const BlockAttnArgs a) {
+  __shared__ unsigned long long warp_sum[32];
+  const int tiles = a.BHk * a.nblk * (a.block / kBaTile);
+  unsigned long long carry = 0;
+  for (int t0 = 0; t0 < tiles; t0 += 1024) {
+    const int t = t0 + threadIdx.x;
+    const int v = t < tiles ? a.item_first[t] : 0;
+    const unsigned long long own = (static_cast<unsigned long long>(v) << 32) | (v > 1 ? v : 0);
+    unsigned long long x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (static_cast<int>(lane_id()) >= o) x += y;
+    }
+    if (lane_id() == 31) warp_sum[warp_id()] = x;
+    __syncthreads();
+    unsigned long long at = carry + x - own;
+    for (int w = 0; w < 32; ++w) {
+      if (w < static_cast<int>(warp_id())) at += warp_sum[w];
+      carry += warp_sum[w];
+    }
+    if (t < tiles) {
+      const int item = static_cast<int>(at >> 32);
+      a.item_first[t] = item;
+      a.slot_first[t] = static_cast<int>(at & 0xFFFFFFFFu);
+      for (int i = 0; i < v; ++i) a.items[item + i] = t;
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.item_first[tiles] = static_cast<int>(carry >> 32);
+}
+
+// dK and dV of one key tile over up to item_tokens of the queries that list its
+// block: 4 warps x 16 keys, 64 gathered (query, head) rows at a time.
+//   S^T = K Q^T, P^T = exp(S^T - lse), dV += P^T dO, dP^T = V dO^T, dK += dS^T Q
+// A tile with one item is stored, others go to fp32 slots summed in order.
+constexpr int kBaRows = 64;
+template <int D>
+__host__ __device__ inline size_t block_attn_dkv_smem(int item_tokens) {
+  return static_cast<size_t>(4) * kBaRows * D * 2 + static_cast<size_t>(2) * kBaRows * 12 +
+         static_cast<size_t>(item_tokens) * 4 + 64;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBaThreads) block_attn_dkv_kernel(const BlockAttnArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int TILE = kBaRows * D * 2, NT = D / 8, COLS = D / 8;
+  const int sub = a.block / kBaTile;
+  const int tiles = a.BHk * a.nblk * sub;
+  const int nitems = a.item_first[tiles];
+  const int item = blockIdx.x;
+  if (item >= nitems) return;
+  const int tile = a.items[item];
+  const int first = a.item_first[tile];
+  const bool alone = a.item_first[tile + 1] - first == 1;
+  const int64_t blk = tile / sub;
+  const int head = static_cast<int>(blk / a.nblk);
+  const int key0 = static_cast<int>(blk % a.nblk) * a.block + (tile % sub) * kBaTile;
+  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
+  const int warp = warp_id(), lane = lane_id();
+  float *row_lse = reinterpret_cast<float *>(smem + 4 * TILE);      // [2][64]
+  float *row_delta = row_lse + 2 * kBaRows;
+  int *row_seen = reinterpret_cast<int *>(row_delta + 2 * kBaRows);
+  int *toks = row_seen + 2 * kBaRows;
+  __shared__ int warp_sum[4];
+
+  // this item's queries: places [skip, skip + item_tokens) of the block's bit set
+  const int skip = (item - first) * a.item_tokens;
+  const int WQ = (a.Nq + 31) / 32;
+  const uint32_t *rev = a.rev + blk * WQ;
+  int carry = 0;
+  for (int w0 = 0; w0 < WQ; w0 += kBaThreads) {
+    const int w = w0 + threadIdx.x;
+    uint32_t u = w < WQ ? rev[w] : 0u;
+    int x = __popc(u);
+    const int own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int at = carry + x - own - skip;
+    for (int i = 0; i < 4; ++i) {
+      if (i < warp) at += warp_sum[i];
+      carry += warp_sum[i];
+    }
+    while (u) {
+      if (at >= 0 && at < a.item_tokens) toks[at] = w * 32 + __ffs(u) - 1;
+      u &= u - 1;
+      ++at;
+    }
+    __syncthreads();
+  }
+  const int ntok = min(max(carry - skip, 0), a.item_tokens);
+  const int rows = ntok * a.G;
+
+  const uint32_t base = smem_u32(smem);
+  const int64_t qbase = static_cast<int64_t>(head) * a.G * a.Nq;
+  auto fetch = [&](int r0, int st) {
+    if (r0 < rows) {
+      const uint32_t qt = base + static_cast<uint32_t>(st) * 2 * TILE, dt = qt + TILE;
+      for (int i = threadIdx.x; i < kBaRows * COLS; i += kBaThreads) {
+        const int r = i / COLS, c = i % COLS;
+        const bool in = r0 + r < rows;
+        const int n = in ? toks[(r0 + r) / a.G] : 0;
+        const int64_t src = (qbase + static_cast<int64_t>((r0 + r) % a.G) * a.Nq + n) * D + 8 * c;
+        cp_async16(qt + tile_at<D>(r, c), a.q + (in ? src : 0), in ? 16u : 0u);
+        cp_async16(dt + tile_at<D>(r, c), a.dout + (in ? src : 0), in ? 16u : 0u);
+      }
+      if (threadIdx.x < kBaRows) {
+        const int r = r0 + threadIdx.x;
+        const bool in = r < rows;
+        const int n = in ? toks[r / a.G] : 0;
+        const int64_t src = qbase + static_cast<int64_t>(r % a.G) * a.Nq + n;
+        row_lse[st * kBaRows + threadIdx.x] = in ? a.lse_in[src] * 1.4426950408889634f : 0.f;
+        row_delta[st * kBaRows + threadIdx.x] = in ? a.delta[src] : 0.f;
+        row_seen[st * kBaRows + threadIdx.x] = in ? query_seen(a, len, n) : 0;
+      }
+    }
+    cp_async_commit();
+  };
+
+  uint32_t kf[D / 16][4], vf[D / 16][4];
+  const int ka = key0 + 16 * warp + frag_row(), kb = ka + 8;
+  {
+    const int64_t hk = static_cast<int64_t>(head) * a.Nk;
+    load_rows<D>(kf, ka < len ? a.k + (hk + ka) * D : nullptr, kb < len ? a.k + (hk + kb) * D : nullptr);
+    load_rows<D>(vf, ka < len ? a.v + (hk + ka) * D : nullptr, kb < len ? a.v + (hk + kb) * D : nullptr);
+  }
+  float dk[NT][4], dv[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) dk[t][e] = dv[t][e] = 0.f;
+
+  fetch(0, 0);
+  for (int r0 = 0, st = 0; r0 < rows; r0 += kBaRows, st ^= 1) {
+    fetch(r0 + kBaRows, st ^ 1);
+    cp_async_wait<1>();
+    __syncthreads();
+    const uint32_t qt = base + static_cast<uint32_t>(st) * 2 * TILE, dt = qt + TILE;
+#pragma unroll 1
+    for (int rs = 0; rs < kBaRows; rs += 16) {
+      if (r0 + rs >= rows) break;
+      float s[2][4], dp[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = dp[t][e] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        uint32_t b[4];
+        ldsm_x4(ldsm_b<D>(qt, rs, ks), b);
+        mma_bf16(s[0], kf[ks], b[0], b[1]);
+        mma_bf16(s[1], kf[ks], b[2], b[3]);
+        ldsm_x4(ldsm_b<D>(dt, rs, ks), b);
+        mma_bf16(dp[0], vf[ks], b[0], b[1]);
+        mma_bf16(dp[1], vf[ks], b[2], b[3]);
+      }
+      uint32_t pf[4], gf[4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        float p[4], g[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = st * kBaRows + rs + 8 * t + frag_col() + (e & 1);
+          const bool in = (e < 2 ? ka : kb) < row_seen[r];
+          p[e] = in ? ex2_approx(s[t][e] * a.scale_log2 - row_lse[r]) : 0.f;
+          g[e] = in ? p[e] * (dp[t][e] - row_delta[r]) : 0.f;
+        }
+        pf[2 * t] = pack_bf16(p[0], p[1]);
+        pf[2 * t + 1] = pack_bf16(p[2], p[3]);
+        gf[2 * t] = pack_bf16(g[0], g[1]);
+        gf[2 * t + 1] = pack_bf16(g[2], g[3]);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; t += 2) {
+        uint32_t b[4];
+        ldsm_x4_trans(ldsm_a<D>(dt, rs, t / 2), b);
+        mma_bf16(dv[t], pf, b[0], b[1]);
+        mma_bf16(dv[t + 1], pf, b[2], b[3]);
+        ldsm_x4_trans(ldsm_a<D>(qt, rs, t / 2), b);
+        mma_bf16(dk[t], gf, b[0], b[1]);
+        mma_bf16(dk[t + 1], gf, b[2], b[3]);
+      }
+    }
+    __syncthreads();
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int key = half ? kb : ka;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int c = 8 * t + frag_col();
+      const float k0 = dk[t][2 * half] * a.scale, k1 = dk[t][2 * half + 1] * a.scale;
+      const float v0 = dv[t][2 * half], v1 = dv[t][2 * half + 1];
+      if (alone) {
+        if (key < a.Nk) {
+          const int64_t at = (static_cast<int64_t>(head) * a.Nk + key) * D + c;
+          *reinterpret_cast<uint32_t *>(a.dk + at) = pack_bf16(k0, k1);
+          *reinterpret_cast<uint32_t *>(a.dv + at) = pack_bf16(v0, v1);
+        }
+      } else {
+        float *slot = a.part_kv + static_cast<int64_t>(a.slot_first[tile] + item - first) * 2 * kBaTile * D +
+                      (key - key0) * D + c;
+        *reinterpret_cast<float2 *>(slot) = make_float2(k0, k1);
+        *reinterpret_cast<float2 *>(slot + kBaTile * D) = make_float2(v0, v1);
+      }
+    }
+  }
+}
+
+// Sum of the items of a key tile with several: one CTA per tile.
+template <int D>
+__global__ void __launch_bounds__(256) block_attn_dkv_join_kernel(const BlockAttnArgs a) {
+  const int sub = a.block / kBaTile;
+  const int tile = blockIdx.x;
+  const int first = a.item_first[tile], last = a.item_first[tile + 1];
+  if (last - first <= 1) return;
+  const int64_t blk = tile / sub;
+  const int head = static_cast<int>(blk / a.nblk);
+  const int key0 = static_cast<int>(blk % a.nblk) * a.block + (tile % sub) * kBaTile;
+  const float *slots = a.part_kv + static_cast<int64_t>(a.slot_first[tile]) * 2 * kBaTile * D;
+  for (int i = threadIdx.x; i < kBaTile * D; i += 256) {          // pairs of channels, dK then dV
+    const int e = 2 * i, which = e / (kBaTile * D), at = e % (kBaTile * D);
+    float2 s = make_float2(0.f, 0.f);
+    for (int it = 0; it < last - first; ++it) {
+      const float2 v = *reinterpret_cast<const float2 *>(slots + static_cast<int64_t>(it) * 2 * kBaTile * D + e);
+      s.x += v.x;
+      s.y += v.y;
+    }
+    const int key = key0 + at / D;
+    if (key < a.Nk)
+      *reinterpret_cast<uint32_t *>((which ? a.dv : a.dk) + (static_cast<int64_t>(head) * a.Nk + key) * D + at % D) =
+          pack_bf16(s.x, s.y);
+  }
+}
+
+}  // namespace svg

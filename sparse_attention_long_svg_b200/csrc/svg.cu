@@ -8,11 +8,14 @@
 #include <mutex>
 
 #include "attn.cuh"
+#include "blockattn.cuh"
+#include "blocksel.cuh"
 #include "common.cuh"
 #include "dynrad.cuh"
 #include "fp8.cuh"
 #include "kmeans.cuh"
 #include "kmeans_tc.cuh"
+#include "rope.cuh"
 #include "select.cuh"
 #include "sort.cuh"
 
@@ -805,3 +808,490 @@ extern "C" svg_status svg_sparse_attn_noalloc(const void *qp, const void *kp, co
   return svg_sparse_attn(qp, kp, vp, BH, N, D, q_off, Cq, k_off, Ck, sel_count, sel_cols, scale, op,
                          lse, ws, SVG_NOALLOC_SCRATCH_BYTES, stream);
 }
+
+// ------------------------------------------------------------------ Q/K norm with rotation
+namespace {
+constexpr int kRopeBackwardTiles = 4 * 148;    // CTAs of the gradient (bounds its partial sums)
+
+// Strides of a token-major view must keep rows on 16-byte boundaries.
+bool rope_strides_ok(const int64_t *s) { return s && s[0] % 8 == 0 && s[1] % 8 == 0 && s[2] % 8 == 0; }
+
+// Shapes shared by both directions; fills everything but the gradients.
+svg_status rope_args(RopeArgs &a, const void *const *x, const int64_t *const *xs, const float *w_q, const float *w_k,
+                     const float *cos, const float *sin, int P, int B, int N, int D, int Hq, int Hk, float eps,
+                     const int32_t *start, int cap) {
+  if (B <= 0 || N <= 0 || Hq <= 0 || Hk < 0 || cap < 0 || !(eps >= 0.f)) return SVG_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return SVG_ERR_UNSUPPORTED;
+  const int64_t heads = static_cast<int64_t>(Hq) + 2ll * Hk;
+  if (static_cast<int64_t>(B) * N * heads >= (1ll << 31) - 1) return SVG_ERR_UNSUPPORTED;
+  if ((cos == nullptr) != (sin == nullptr) || (cos && P <= 0)) return SVG_ERR_INVALID_ARG;
+  if (cos && (!aligned(cos, 16) || !aligned(sin, 16))) return SVG_ERR_INVALID_ARG;
+  a = RopeArgs{};
+  a.w[0] = w_q;
+  a.w[1] = w_k;
+  a.cos = cos;
+  a.sin = sin;
+  a.start = start;
+  a.B = B;
+  a.N = N;
+  a.P = P;
+  a.eps = eps;
+  for (int t = 0; t < 3; ++t) {
+    a.heads[t] = t == 0 ? Hq : Hk;
+    a.cap[t] = t == 0 ? N : cap;
+    if (x[t] == nullptr) a.heads[t] = 0;
+    if (a.heads[t] == 0) continue;
+    if (!aligned(x[t], 16) || !rope_strides_ok(xs[t])) return SVG_ERR_INVALID_ARG;
+    a.x[t] = static_cast<const __nv_bfloat16 *>(x[t]);
+    a.xb[t] = xs[t][0];
+    a.xn[t] = xs[t][1];
+    a.xh[t] = xs[t][2];
+  }
+  return SVG_OK;
+}
+
+void rope_chunks(RopeArgs &a, int hpt) {
+  a.hpt = hpt;
+  for (int t = 0; t < 3; ++t) a.chunks[t] = (a.heads[t] + hpt - 1) / hpt;
+}
+
+// Heads of a CTA's chunk in the gradient, and its token tiles.
+int rope_backward_heads(int Hq, int Hk) { return Hq + Hk > 16 ? 8 : 4; }
+int rope_backward_tiles(int B, int N, int D, int chunks) {
+  const int64_t groups = kRopeThreads / (D / 16);
+  const int64_t tiles = (static_cast<int64_t>(B) * N + groups - 1) / groups;
+  const int64_t most = (kRopeBackwardTiles + chunks - 1) / chunks;
+  return static_cast<int>(tiles < most ? tiles : most);
+}
+}  // namespace
+
+extern "C" {
+
+svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                            const void *v, const int64_t *v_strides, const float *w_q, const float *w_k,
+                            const float *cos, const float *sin, int P, int B, int N, int Hq, int Hk, int D, float eps,
+                            int interleaved, const int32_t *start, void *q_out, void *k_out, void *v_out, int cap,
+                            svg_stream_t stream) {
+  const void *x[3] = {q, k, v};
+  const int64_t *xs[3] = {q_strides, k_strides, v_strides};
+  void *y[3] = {q_out, k_out, v_out};
+  if (!q || !q_out || (interleaved & ~1)) return SVG_ERR_INVALID_ARG;
+  RopeArgs a;
+  svg_status st = rope_args(a, x, xs, w_q, w_k, cos, sin, P, B, N, D, Hq, Hk, eps, start, cap);
+  if (st != SVG_OK) return st;
+  for (int t = 0; t < 3; ++t) {
+    if (a.heads[t] == 0) continue;
+    if (!y[t] || !aligned(y[t], 16) || y[t] == x[t]) return SVG_ERR_INVALID_ARG;
+    if (t > 0 && !start && cap < N) return SVG_ERR_INVALID_ARG;
+    a.y[t] = static_cast<__nv_bfloat16 *>(y[t]);
+  }
+  if (cos && !start && P < N) return SVG_ERR_INVALID_ARG;
+  // One head per thread while that leaves the GPU short of threads, else 4 in
+  // flight of a chunk of 8 that shares its angles.
+  const int64_t rows = static_cast<int64_t>(B) * N * (a.heads[0] + a.heads[1] + a.heads[2]);
+  const bool wide = rows * (D / 16) >= static_cast<int64_t>(num_sms()) * 2048 * 4;
+  rope_chunks(a, wide ? 8 : 1);
+  const int64_t groups = static_cast<int64_t>(B) * N * (a.chunks[0] + a.chunks[1] + a.chunks[2]);
+  const int64_t per = kRopeThreads / (D / 16);
+  const unsigned grid = static_cast<unsigned>((groups + per - 1) / per);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto few, auto many) {
+    if (wide)
+      many<<<grid, kRopeThreads, 0, s>>>(a);
+    else
+      few<<<grid, kRopeThreads, 0, s>>>(a);
+  };
+  if (D == 128)
+    interleaved ? go(qk_norm_rope_kernel<128, true, 1>, qk_norm_rope_kernel<128, true, 4>)
+                : go(qk_norm_rope_kernel<128, false, 1>, qk_norm_rope_kernel<128, false, 4>);
+  else
+    interleaved ? go(qk_norm_rope_kernel<64, true, 1>, qk_norm_rope_kernel<64, true, 4>)
+                : go(qk_norm_rope_kernel<64, false, 1>, qk_norm_rope_kernel<64, false, 4>);
+  return launch_status("qk_norm_rope_kernel");
+}
+
+size_t svg_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, int D) {
+  if (B <= 0 || N <= 0 || Hq <= 0 || Hk < 0 || (D != 64 && D != 128)) return 0;
+  const int hpt = rope_backward_heads(Hq, Hk);
+  const int cq = (Hq + hpt - 1) / hpt, ck = (Hk + hpt - 1) / hpt;
+  return align256(static_cast<size_t>(cq + ck) * rope_backward_tiles(B, N, D, cq + ck) * D * sizeof(float));
+}
+
+svg_status svg_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *dv_out, const void *q,
+                                     const int64_t *q_strides, const void *k, const int64_t *k_strides,
+                                     const float *w_q, const float *w_k, const float *cos, const float *sin, int P,
+                                     int B, int N, int Hq, int Hk, int D, float eps, int interleaved,
+                                     const int32_t *start, int cap, void *dq, const int64_t *dq_strides, void *dk,
+                                     const int64_t *dk_strides, void *dv, const int64_t *dv_strides, float *dw_q,
+                                     float *dw_k, void *ws, size_t ws_bytes, svg_stream_t stream) {
+  const void *dy[3] = {dq_out, dk_out, dv_out};
+  void *dx[3] = {dq, dk, dv};
+  const int64_t *ds[3] = {dq_strides, dk_strides, dv_strides};
+  // V's rows are only moved: its place in the checks is taken by its gradient
+  const void *x[3] = {q, k, dv};
+  const int64_t *xs[3] = {q_strides, k_strides, dv_strides};
+  if (!q || !dq_out || !dq || !ws || (interleaved & ~1)) return SVG_ERR_INVALID_ARG;
+  RopeArgs a;
+  svg_status st = rope_args(a, x, xs, w_q, w_k, cos, sin, P, B, N, D, Hq, Hk, eps, start, cap);
+  if (st != SVG_OK) return st;
+  for (int t = 0; t < 3; ++t) {
+    if (a.heads[t] == 0) continue;
+    if (!dy[t] || !dx[t] || !aligned(dy[t], 16) || !aligned(dx[t], 16) || !rope_strides_ok(ds[t]))
+      return SVG_ERR_INVALID_ARG;
+    if (dx[t] == dy[t]) return SVG_ERR_INVALID_ARG;
+    if (t > 0 && !start && cap < N) return SVG_ERR_INVALID_ARG;
+    a.dy[t] = static_cast<const __nv_bfloat16 *>(dy[t]);
+    a.dx[t] = static_cast<__nv_bfloat16 *>(dx[t]);
+    a.db[t] = ds[t][0];
+    a.dn[t] = ds[t][1];
+    a.dh[t] = ds[t][2];
+  }
+  if (cos && !start && P < N) return SVG_ERR_INVALID_ARG;
+  if (!aligned(ws, 256)) return SVG_ERR_INVALID_ARG;
+  if (ws_bytes < svg_qk_norm_rope_backward_workspace_size(B, N, Hq, Hk, D)) return SVG_ERR_WORKSPACE;
+  rope_chunks(a, rope_backward_heads(Hq, Hk));
+  a.partial = static_cast<float *>(ws);
+  const int tiles = rope_backward_tiles(B, N, D, (Hq + a.hpt - 1) / a.hpt + (Hk + a.hpt - 1) / a.hpt);
+  const dim3 grid(tiles, a.chunks[0] + a.chunks[1] + a.chunks[2]);
+  if (grid.y > 65535u) return SVG_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto kernel) { kernel<<<grid, kRopeThreads, 0, s>>>(a); };
+  if (D == 128)
+    interleaved ? go(qk_norm_rope_backward_kernel<128, true>) : go(qk_norm_rope_backward_kernel<128, false>);
+  else
+    interleaved ? go(qk_norm_rope_backward_kernel<64, true>) : go(qk_norm_rope_backward_kernel<64, false>);
+  st = launch_status("qk_norm_rope_backward_kernel");
+  if (st != SVG_OK || (!dw_q && !dw_k)) return st;
+  const int rows_q = a.chunks[0] * tiles, rows_k = a.chunks[1] * tiles;
+  if (D == 128)
+    rope_dw_kernel<128><<<dim3(16, 2), 256, 0, s>>>(a.partial, rows_q, rows_k, dw_q, dw_k);
+  else
+    rope_dw_kernel<64><<<dim3(8, 2), 256, 0, s>>>(a.partial, rows_q, rows_k, dw_q, dw_k);
+  return launch_status("rope_dw_kernel");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ blocks chosen for each query
+namespace {
+// Shapes shared by the calls; nblk gets the blocks of a buffer.
+svg_status block_shapes(int BHq, int BHk, int B, int Nq, int Nk, int D, int block, int *nblk) {
+  if (BHq <= 0 || BHk <= 0 || B <= 0 || Nq <= 0 || Nk <= 0 || BHq % BHk != 0 || BHk % B != 0)
+    return SVG_ERR_INVALID_ARG;
+  if (!sizes_ok(BHq, Nq) || !sizes_ok(BHk, Nk)) return SVG_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return SVG_ERR_UNSUPPORTED;
+  if (block != 64 && block != 128) return SVG_ERR_UNSUPPORTED;
+  if (BHq / BHk > kBaMaxGroup) return SVG_ERR_UNSUPPORTED;
+  *nblk = (Nk + block - 1) / block;
+  return *nblk > kMaxBlocks ? SVG_ERR_UNSUPPORTED : SVG_OK;
+}
+
+// block_select: few queries take the kernel with one CTA per query (it reads a
+// head's means once per query), more the one with 64 queries per CTA.
+bool select_few(int Nq) { return Nq <= 4; }
+int select_ctas(int BHk, int Nq) {
+  const int64_t items = static_cast<int64_t>(BHk) * ((Nq + kSelTile - 1) / kSelTile);
+  const int64_t most = 3ll * num_sms();
+  return static_cast<int>(items < most ? items : most);
+}
+
+struct BlockAttnPlan {
+  bool few;
+  int tokens, tiles, splits;
+};
+// Few CTAs: the union of a tile's blocks is split until the GPU is full, at
+// least 4 tiles to a part.
+BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int block) {
+  BlockAttnPlan p;
+  const int per = 16 / (BHq / BHk);
+  p.few = Nq <= per;
+  p.tokens = p.few ? per : 4 * per;
+  p.tiles = (Nq + p.tokens - 1) / p.tokens;
+  const int64_t ctas = static_cast<int64_t>(BHk) * p.tiles;
+  const int64_t listed = static_cast<int64_t>(Nq < p.tokens ? Nq : p.tokens) * topk;
+  const int64_t keys = (listed < nblk ? listed : nblk) * (block / kBaTile);
+  const int64_t target = (p.few ? 1ll : 2ll) * num_sms();
+  int64_t s = (target + ctas - 1) / ctas;
+  if (s > (keys + 3) / 4) s = (keys + 3) / 4;
+  if (s > kBaMaxSplits) s = kBaMaxSplits;
+  p.splits = static_cast<int>(s < 1 ? 1 : s);
+  return p;
+}
+
+// Gradient: rows of one work item (a key tile's queries beyond it go to more).
+constexpr int kBaItemRows = 2048;
+struct BlockGradWs {
+  float *delta, *part_kv;
+  uint32_t *rev;
+  int32_t *item_first, *slot_first, *items;
+  size_t rev_bytes;
+  int item_tokens;
+  int64_t max_items;
+};
+BlockGradWs carve_block_grad(void *ws, int BHq, int BHk, int Nq, int nblk, int D, int topk, int block, size_t *bytes) {
+  Carve c{static_cast<uint8_t *>(ws)};
+  BlockGradWs w;
+  const int sub = block / kBaTile;
+  const int64_t tiles = static_cast<int64_t>(BHk) * nblk * sub;
+  const int64_t listed = static_cast<int64_t>(BHk) * Nq * (topk < nblk ? topk : nblk) * sub;
+  w.item_tokens = kBaItemRows / (BHq / BHk);
+  w.max_items = tiles + listed / w.item_tokens;
+  w.rev_bytes = static_cast<size_t>(BHk) * nblk * ((Nq + 31) / 32) * 4;
+  w.delta = c.take<float>(static_cast<size_t>(BHq) * Nq);
+  w.rev = reinterpret_cast<uint32_t *>(c.take<uint8_t>(w.rev_bytes));
+  w.item_first = c.take<int32_t>(tiles + 1);
+  w.slot_first = c.take<int32_t>(tiles);
+  w.items = c.take<int32_t>(w.max_items);
+  // tiles with several items: ceil(c / t) <= 2 c / t
+  w.part_kv = c.take<float>(2 * (listed / w.item_tokens) * 2 * kBaTile * static_cast<size_t>(D));
+  *bytes = c.used;
+  return w;
+}
+
+void block_attn_args(BlockAttnArgs &a, const void *q, const void *k, const void *v, int BHq, int BHk, int B, int Nq,
+                     int Nk, int D, int nblk, const int32_t *sel, int topk, int block, int causal, float scale,
+                     const int32_t *kv_len) {
+  a = BlockAttnArgs{};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.k = static_cast<const __nv_bfloat16 *>(k);
+  a.v = static_cast<const __nv_bfloat16 *>(v);
+  a.sel = sel;
+  a.kv_len = kv_len;
+  a.BHk = BHk;
+  a.G = BHq / BHk;
+  a.heads_per_seq = BHk / B;
+  a.Nq = Nq;
+  a.Nk = Nk;
+  a.nblk = nblk;
+  a.block = block;
+  a.topk = topk;
+  a.causal = causal;
+  a.splits = 1;
+  a.scale = scale > 0.f ? scale : 1.f / std::sqrt(static_cast<float>(D));
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+}
+}  // namespace
+
+extern "C" {
+
+svg_status svg_block_mean(const void *k, int BHk, int B, int Nk, int D, int block, const int32_t *kv_len, int fresh,
+                          float *mean, svg_stream_t stream) {
+  if (!k || !mean || fresh < 0 || !aligned(k, 16) || !aligned(mean, 16)) return SVG_ERR_INVALID_ARG;
+  int nblk;
+  svg_status st = block_shapes(BHk, BHk, B, 1, Nk, D, block, &nblk);
+  if (st != SVG_OK) return st;
+  int64_t per = nblk;
+  if (fresh > 0 && (static_cast<int64_t>(fresh) + block - 2) / block + 1 < per) per = (fresh + block - 2) / block + 1;
+  if (per * BHk >= (1ll << 31)) return SVG_ERR_UNSUPPORTED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(k);
+  const unsigned grid = static_cast<unsigned>(per * BHk);
+  if (D == 128)
+    block_mean_kernel<128><<<grid, 256, 0, s>>>(kb, Nk, block, nblk, kv_len, BHk / B, fresh, static_cast<int>(per), mean);
+  else
+    block_mean_kernel<64><<<grid, 256, 0, s>>>(kb, Nk, block, nblk, kv_len, BHk / B, fresh, static_cast<int>(per), mean);
+  return launch_status("block_mean_kernel");
+}
+
+size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int block) {
+  if (BHk <= 0 || Nq <= 0 || Nk <= 0 || block <= 0 || !sizes_ok(BHk, Nq)) return 0;
+  if (select_few(Nq)) return 0;
+  const size_t nblk = (static_cast<size_t>(Nk) + block - 1) / block;
+  return align256(static_cast<size_t>(select_ctas(BHk, Nq)) * nblk *
+                  (kSelTile * sizeof(float) + kSelThreads / 32 * sizeof(double)));
+}
+
+svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, int B, int Nq, int Nk, int D, int block,
+                            int topk, int sink, int local, int causal, const int32_t *kv_len, int32_t *sel, void *ws,
+                            size_t ws_bytes, svg_stream_t stream) {
+  if (!q || !mean || !sel || (causal & ~1)) return SVG_ERR_INVALID_ARG;
+  // the causal block of the query itself holds later keys, so it is taken, not scored
+  if (topk < 1 || sink < 0 || local < causal || static_cast<int64_t>(sink) + local > topk) return SVG_ERR_INVALID_ARG;
+  int nblk;
+  svg_status st = block_shapes(BHq, BHk, B, Nq, Nk, D, block, &nblk);
+  if (st != SVG_OK) return st;
+  if (topk > kMaxBlockTopk) return SVG_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(mean, 16) || !aligned(ws, 256)) return SVG_ERR_INVALID_ARG;
+  const size_t need = svg_block_select_workspace_size(BHk, Nq, Nk, block);
+  if (need > 0 && !ws) return SVG_ERR_INVALID_ARG;
+  if (ws_bytes < need) return SVG_ERR_WORKSPACE;
+  SelectArgs a{};
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.mean = mean;
+  a.kv_len = kv_len;
+  a.sel = sel;
+  a.BHk = BHk;
+  a.G = BHq / BHk;
+  a.heads_per_seq = BHk / B;
+  a.Nq = Nq;
+  a.Nk = Nk;
+  a.nblk = nblk;
+  a.block = block;
+  a.topk = topk;
+  a.sink = sink;
+  a.local = local;
+  a.causal = causal;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool few = select_few(Nq);
+  const int ctas = few ? BHk * Nq : select_ctas(BHk, Nq);
+  if (!few) {
+    a.exact = static_cast<double *>(ws);
+    a.scores = reinterpret_cast<float *>(a.exact + static_cast<size_t>(ctas) * (kSelThreads / 32) * nblk);
+  }
+  auto go = [&](auto one, auto many, size_t tile_bytes) {
+    if (few) {
+      const size_t smem = static_cast<size_t>(nblk) * (sizeof(double) + sizeof(float));
+      if (!set_smem(one, smem)) return SVG_ERR_CUDA;
+      one<<<ctas, kSelDecodeThreads, smem, s>>>(a);
+    } else {
+      if (!set_smem(many, tile_bytes)) return SVG_ERR_CUDA;
+      many<<<ctas, kSelThreads, tile_bytes, s>>>(a);
+    }
+    return launch_status("block_select_kernel");
+  };
+  if (D == 128) {
+    if (nblk <= 256) return go(block_select_decode_kernel<128, 8>, block_select_kernel<128, 8>, select_smem<128>());
+    if (nblk <= 1024) return go(block_select_decode_kernel<128, 32>, block_select_kernel<128, 32>, select_smem<128>());
+    return go(block_select_decode_kernel<128, 128>, block_select_kernel<128, 128>, select_smem<128>());
+  }
+  if (nblk <= 256) return go(block_select_decode_kernel<64, 8>, block_select_kernel<64, 8>, select_smem<64>());
+  if (nblk <= 1024) return go(block_select_decode_kernel<64, 32>, block_select_kernel<64, 32>, select_smem<64>());
+  return go(block_select_decode_kernel<64, 128>, block_select_kernel<64, 128>, select_smem<64>());
+}
+
+size_t svg_block_attn_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block) {
+  int nblk;
+  if (topk < 1 || block_shapes(BHq, BHk, 1, Nq, Nk, D, block, &nblk) != SVG_OK) return 0;
+  const BlockAttnPlan p = block_attn_plan(BHq, BHk, Nq, nblk, topk, block);
+  if (p.splits == 1) return 0;
+  const size_t rows = static_cast<size_t>(BHq) * Nq * p.splits;
+  return align256(rows * D * sizeof(float)) + align256(rows * sizeof(float));
+}
+
+svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, int BHk, int B, int Nq, int Nk, int D,
+                          const int32_t *sel, int topk, int block, int causal, float scale, const int32_t *kv_len,
+                          void *o, float *lse, void *ws, size_t ws_bytes, svg_stream_t stream) {
+  if (!q || !k || !v || !sel || !o || (causal & ~1) || topk < 1) return SVG_ERR_INVALID_ARG;
+  int nblk;
+  svg_status st = block_shapes(BHq, BHk, B, Nq, Nk, D, block, &nblk);
+  if (st != SVG_OK) return st;
+  if (topk > kMaxBlockTopk) return SVG_ERR_UNSUPPORTED;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(ws, 256))
+    return SVG_ERR_INVALID_ARG;
+  if (o == q || o == k || o == v) return SVG_ERR_INVALID_ARG;
+  const size_t need = svg_block_attn_workspace_size(BHq, BHk, Nq, Nk, D, topk, block);
+  if (need > 0 && !ws) return SVG_ERR_INVALID_ARG;
+  if (ws_bytes < need) return SVG_ERR_WORKSPACE;
+  BlockAttnArgs a;
+  block_attn_args(a, q, k, v, BHq, BHk, B, Nq, Nk, D, nblk, sel, topk, block, causal, scale, kv_len);
+  const BlockAttnPlan p = block_attn_plan(BHq, BHk, Nq, nblk, topk, block);
+  a.o = static_cast<__nv_bfloat16 *>(o);
+  a.lse = lse;
+  a.splits = p.splits;
+  if (p.splits > 1) {
+    Carve c{static_cast<uint8_t *>(ws)};
+    a.part_o = c.take<float>(static_cast<size_t>(BHq) * Nq * p.splits * D);
+    a.part_lse = c.take<float>(static_cast<size_t>(BHq) * Nq * p.splits);
+  }
+  const int64_t ctas = static_cast<int64_t>(BHk) * p.tiles;
+  if (ctas >= (1ll << 31)) return SVG_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>(ctas), p.splits);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  auto go = [&](auto kernel, size_t smem) {
+    if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
+    kernel<<<grid, kBaThreads, smem, s>>>(a);
+    return launch_status("block_attn_kernel");
+  };
+  if (D == 128)
+    st = p.few ? go(block_attn_kernel<128, true>, block_attn_smem<128>(8, p.tokens, nblk))
+               : go(block_attn_kernel<128, false>, block_attn_smem<128>(4, p.tokens, nblk));
+  else
+    st = p.few ? go(block_attn_kernel<64, true>, block_attn_smem<64>(8, p.tokens, nblk))
+               : go(block_attn_kernel<64, false>, block_attn_smem<64>(4, p.tokens, nblk));
+  if (st != SVG_OK || p.splits == 1) return st;
+  const unsigned join = static_cast<unsigned>((static_cast<int64_t>(BHq) * Nq + 3) / 4);
+  if (D == 128)
+    block_attn_join_kernel<128><<<join, 128, 0, s>>>(a);
+  else
+    block_attn_join_kernel<64><<<join, 128, 0, s>>>(a);
+  return launch_status("block_attn_join_kernel");
+}
+
+size_t svg_block_attn_backward_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block) {
+  int nblk;
+  if (topk < 1 || block_shapes(BHq, BHk, 1, Nq, Nk, D, block, &nblk) != SVG_OK) return 0;
+  size_t bytes = 0;
+  carve_block_grad(nullptr, BHq, BHk, Nq, nblk, D, topk, block, &bytes);
+  return bytes;
+}
+
+svg_status svg_block_attn_backward(const void *dout, const void *q, const void *k, const void *v, const void *o,
+                                   const float *lse, int BHq, int BHk, int B, int Nq, int Nk, int D,
+                                   const int32_t *sel, int topk, int block, int causal, float scale,
+                                   const int32_t *kv_len, void *dq, void *dk, void *dv, void *ws, size_t ws_bytes,
+                                   svg_stream_t stream) {
+  if (!dout || !q || !k || !v || !o || !lse || !sel || !dq || !dk || !dv || !ws || (causal & ~1) || topk < 1)
+    return SVG_ERR_INVALID_ARG;
+  int nblk;
+  svg_status st = block_shapes(BHq, BHk, B, Nq, Nk, D, block, &nblk);
+  if (st != SVG_OK) return st;
+  if (topk > kMaxBlockTopk) return SVG_ERR_UNSUPPORTED;
+  const void *in[5] = {dout, q, k, v, o};
+  void *out[3] = {dq, dk, dv};
+  for (const void *x : in)
+    if (!aligned(x, 16)) return SVG_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    if (!aligned(out[i], 16) || out[i] == out[(i + 1) % 3]) return SVG_ERR_INVALID_ARG;
+    for (const void *x : in)
+      if (out[i] == x) return SVG_ERR_INVALID_ARG;
+  }
+  if (!aligned(ws, 256)) return SVG_ERR_INVALID_ARG;
+  size_t need = 0;
+  const BlockGradWs w = carve_block_grad(ws, BHq, BHk, Nq, nblk, D, topk, block, &need);
+  if (ws_bytes < need) return SVG_ERR_WORKSPACE;
+  const int sub = block / kBaTile;
+  const int64_t tiles = static_cast<int64_t>(BHk) * nblk * sub;
+  const int64_t listed = static_cast<int64_t>(BHk) * Nq * topk;
+  const int tokens = 4 * (16 / (BHq / BHk));
+  const int64_t ctas = static_cast<int64_t>(BHk) * ((Nq + tokens - 1) / tokens);
+  if (tiles >= (1ll << 31) - 1 || w.max_items >= (1ll << 31) - 1 || (listed + 255) / 256 >= (1ll << 31) ||
+      ctas >= (1ll << 31))
+    return SVG_ERR_UNSUPPORTED;
+  BlockAttnArgs a;
+  block_attn_args(a, q, k, v, BHq, BHk, B, Nq, Nk, D, nblk, sel, topk, block, causal, scale, kv_len);
+  a.dout = static_cast<const __nv_bfloat16 *>(dout);
+  a.out = static_cast<const __nv_bfloat16 *>(o);
+  a.lse_in = lse;
+  a.delta = w.delta;
+  a.dq = static_cast<__nv_bfloat16 *>(dq);
+  a.dk = static_cast<__nv_bfloat16 *>(dk);
+  a.dv = static_cast<__nv_bfloat16 *>(dv);
+  a.rev = w.rev;
+  a.item_first = w.item_first;
+  a.slot_first = w.slot_first;
+  a.items = w.items;
+  a.part_kv = w.part_kv;
+  a.item_tokens = w.item_tokens;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = cuda_status(cudaMemsetAsync(w.rev, 0, w.rev_bytes, s), "cudaMemsetAsync(block lists)");
+  if (st != SVG_OK) return st;
+  block_attn_reverse_kernel<<<static_cast<unsigned>((listed + 255) / 256), 256, 0, s>>>(a);
+  block_attn_count_kernel<<<static_cast<unsigned>((static_cast<int64_t>(BHk) * nblk + 7) / 8), 256, 0, s>>>(a);
+  block_attn_items_kernel<<<1, 1024, 0, s>>>(a);
+  st = launch_status("block_attn_items_kernel");
+  if (st != SVG_OK) return st;
+  auto go = [&](auto dq_kernel, size_t dq_smem, auto dkv_kernel, size_t dkv_smem, auto join) {
+    if (!set_smem(dq_kernel, dq_smem) || !set_smem(dkv_kernel, dkv_smem)) return SVG_ERR_CUDA;
+    dq_kernel<<<static_cast<unsigned>(ctas), kBaThreads, dq_smem, s>>>(a);
+    dkv_kernel<<<static_cast<unsigned>(w.max_items), kBaThreads, dkv_smem, s>>>(a);
+    join<<<static_cast<unsigned>(tiles), 256, 0, s>>>(a);
+    return launch_status("block_attn gradient kernels");
+  };
+  if (D == 128)
+    return go(block_attn_dq_kernel<128>, block_attn_smem<128>(4, tokens, nblk), block_attn_dkv_kernel<128>,
+              block_attn_dkv_smem<128>(w.item_tokens), block_attn_dkv_join_kernel<128>);
+  return go(block_attn_dq_kernel<64>, block_attn_smem<64>(4, tokens, nblk), block_attn_dkv_kernel<64>,
+            block_attn_dkv_smem<64>(w.item_tokens), block_attn_dkv_join_kernel<64>);
+}
+
+}  // extern "C"
