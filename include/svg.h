@@ -398,7 +398,7 @@ svg_status svg_block_mean(const void *k, int BHk, int B, int Nk, int D, int bloc
  * own are taken, the rest by score (NaN counts as -inf), the lower block on a
  * tie, until topk are listed.  The choice is the one of exact (fp64) scores.
  * Requires sink + local <= topk, and local >= 1 when causal. */
-size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int block);
+size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int D, int block);
 svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, int B, int Nq, int Nk, int D,
                             int block, int topk, int sink, int local, int causal, const int32_t *kv_len,
                             int32_t *sel, void *ws, size_t ws_bytes, svg_stream_t stream);

@@ -73,7 +73,7 @@ SIGNATURES = {
     "svg_qk_norm_rope_backward_workspace_size": (_SZ, [_I] * 5),
     "svg_qk_norm_rope_backward": (_I, [_P] * 11 + [_I] * 6 + [_F, _I, _P, _I] + [_P] * 9 + [_SZ, _P]),
     "svg_block_mean": (_I, [_P, _I, _I, _I, _I, _I, _P, _I, _P, _P]),
-    "svg_block_select_workspace_size": (_SZ, [_I] * 4),
+    "svg_block_select_workspace_size": (_SZ, [_I] * 5),
     "svg_block_select": (_I, [_P, _P] + [_I] * 11 + [_P, _P, _P, _SZ, _P]),
     "svg_block_attn_workspace_size": (_SZ, [_I] * 7),
     "svg_block_attn": (_I, [_P] * 3 + [_I] * 6 + [_P, _I, _I, _I, _F, _P, _P, _P, _P, _SZ, _P]),

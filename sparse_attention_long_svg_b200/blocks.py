@@ -290,8 +290,8 @@ def block_select(q: torch.Tensor, mean: torch.Tensor, block: int, topk: int, Nk:
     _same(mean, "mean", (BHk, -(-Nk // block), D), torch.float32)
     with _side(stream, q, mean, kv_len, sel, workspace):
         sel = _out(sel, "sel", (BHk, Nq, topk), torch.int32, q.device)
-        workspace, nbytes = _scratch(workspace, lib.svg_block_select_workspace_size(BHk, Nq, int(Nk), int(block)),
-                                     q.device)
+        workspace, nbytes = _scratch(
+            workspace, lib.svg_block_select_workspace_size(BHk, Nq, int(Nk), D, int(block)), q.device)
         _check("svg_block_select", lib.svg_block_select(
             _ptr(q), _ptr(mean), BHq, BHk, B, Nq, int(Nk), D, int(block), int(topk), int(sink), int(local),
             1 if causal else 0, _ptr(kv_len), _ptr(sel), _ptr(workspace), nbytes, _stream()))

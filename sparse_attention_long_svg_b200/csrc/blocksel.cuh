@@ -68,7 +68,10 @@ struct SelectArgs {
   const float *mean;                   // [BHk, nblk, D]
   const int32_t *kv_len;
   int32_t *sel;                        // [BHk, Nq, topk]
-  float *scores;                       // prefill: per CTA [64][nblk]
+  // many queries only (workspace):
+  __nv_bfloat16 *mean_hi, *mean_lo;    // [BHk, nblk up to whole tiles, D]: the means' bf16 parts
+  float *tile_norm;                    // [BHk, tiles] largest |mean|^2 of a tile
+  float *scores;                       // per CTA [64][nblk]
   double *exact;                       // per warp [nblk]
   int BHk, G, heads_per_seq, Nq, Nk, nblk, block, topk, sink, local, causal;
 };
@@ -106,7 +109,7 @@ __device__ __forceinline__ SelectRange select_range(const SelectArgs &a, int len
   return r;
 }
 
-// Exact score of block j: every lane returns it.
+// Exact score of block j from the lane's summed query channels: every lane returns it.
 template <int D>
 __device__ __forceinline__ double exact_score(const SelectArgs &a, const double (&qs)[D / 32], int head, int j) {
   const float *m = a.mean + (static_cast<int64_t>(head) * a.nblk + j) * D + lane_id() * (D / 32);
@@ -116,6 +119,36 @@ __device__ __forceinline__ double exact_score(const SelectArgs &a, const double 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
+}
+template <int D>
+__device__ __forceinline__ void exact_query(const SelectArgs &a, double (&qs)[D / 32], int head, int n) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    qs[i] = 0.0;
+    for (int g = 0; g < a.G; ++g)
+      qs[i] += static_cast<double>(__bfloat162float(
+          a.q[((static_cast<int64_t>(head) * a.G + g) * a.Nq + n) * D + lane_id() * (D / 32) + i]));
+  }
+}
+
+// A thread's share of a squared norm: not below a floor where any value is not
+// zero, so that squares which underflow cannot make the error bound too small
+// (and a bound of zero means that every score is zero).  NaN stays.
+constexpr float kNormFloor = 1e-28f;
+template <int E>
+__device__ __forceinline__ float norm_part(float sum, const float (&v)[E]) {
+  bool none = true;
+#pragma unroll
+  for (int e = 0; e < E; ++e) none = none && v[e] == 0.f;
+  return none ? 0.f : sum < kNormFloor ? kNormFloor : sum;
+}
+
+// Where an approximate score stands against the last place's, t: above (in),
+// near (to be compared exactly), else out.  Written so that an infinite bound
+// or a NaN makes everything near.
+__device__ __forceinline__ bool score_above(float f, float t, float bound) { return f > t + 2.f * bound; }
+__device__ __forceinline__ bool score_near(float f, float t, float bound) {
+  return !score_above(f, t, bound) && !(f < t - 2.f * bound);
 }
 
 // One warp writes one query's list.  s: approximate scores of the blocks
@@ -135,13 +168,23 @@ __device__ void select_row(const SelectArgs &a, const float *s, double *exact, f
     const int j = i * 32 + lane;
     key[i] = (i < places && j < r.may && !r.forced(j)) ? key32(s[j]) : 0u;
   }
-  // keep = key >= low (key 0 never is), and ties of the border resolved below
-  uint32_t low = 1;
+  uint32_t low = 1;                    // without a border: keep = key >= low (key 0 never is)
   bool border = false;
   float t = 0.f;
   if (r.may - forced > need) {
-    uint32_t cut = 0;
-    for (int bit = 31; bit >= 0; --bit) {
+    // The need-th largest key, bit by bit.  While need <= 32, the smallest of
+    // the lanes' largest keys bounds it from below, so the bits that this
+    // bound shares with the largest key are known.
+    uint32_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i < places) mine = max(mine, key[i]);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, mine);
+    const uint32_t floor = need <= 32 ? __reduce_min_sync(0xffffffffu, mine) : 0u;
+    const uint32_t open = top ^ floor;
+    int bit = open ? 31 - __clz(open) : -1;
+    uint32_t cut = bit < 0 ? top : bit == 31 ? 0u : (top >> (bit + 1)) << (bit + 1);
+    for (; bit >= 0; --bit) {
       const uint32_t trial = cut | (1u << bit);
       int c = 0;
 #pragma unroll
@@ -163,74 +206,106 @@ __device__ void select_row(const SelectArgs &a, const float *s, double *exact, f
     for (int i = 0; i < VPL; ++i)
       if (i < places && key[i] != 0) {
         const float f = unkey32(key[i]);
-        const bool above = f > t + 2.f * bound;
-        sure += above;
-        near += !above && !(f < t - 2.f * bound);
+        sure += score_above(f, t, bound);
+        near += score_near(f, t, bound);
       }
-    sure = __reduce_add_sync(0xffffffffu, sure);
-    near = __reduce_add_sync(0xffffffffu, near);
+    const int both = __reduce_add_sync(0xffffffffu, sure | (near << 16));
+    sure = both & 0xFFFF;
+    near = both >> 16;
     border = need > 0 && sure + near > need;
-    need -= sure;
-  }
-  uint64_t cut64 = 0;
-  int ties = 0;
-  if (border) {
-    double qs[D / 32];
+    if (border) {
+      need -= sure;
+      // near ones get key 1 where they stay, 0 where not; all others are kept or 0
+      double qs[D / 32];
+      if (bound > 0.f) exact_query<D>(a, qs, head, n);
+      if (near <= 32 || !(bound > 0.f)) {
+        // up to 32: lane c holds the c-th one and ranks it against the others.
+        // A bound of zero (query or means of zero): all tie, the first ones stay.
+        double v = 0.0;
+        int at = 0;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      qs[i] = 0.0;
-      for (int g = 0; g < a.G; ++g)
-        qs[i] += static_cast<double>(
-            __bfloat162float(a.q[((static_cast<int64_t>(head) * a.G + g) * a.Nq + n) * D + lane * (D / 32) + i]));
-    }
+        for (int i = 0; i < VPL; ++i) {
+          if (i >= places) break;
+          const bool is = key[i] != 0 && score_near(unkey32(key[i]), t, bound);
+          uint32_t m = __ballot_sync(0xffffffffu, is);
+          if (!(bound > 0.f)) {
+            if (is) key[i] = at + __popc(m & ((1u << lane) - 1)) < need ? 1u : 0u;
+            at += __popc(m);
+            continue;
+          }
+          if (is) key[i] = 2u + at + __popc(m & ((1u << lane) - 1));    // its holder
+          for (; m; m &= m - 1, ++at) {
+            double x = exact_score<D>(a, qs, head, i * 32 + __ffs(m) - 1);
+            if (x != x) x = -INFINITY;
+            if (lane == at) v = x;
+          }
+        }
+        if (bound > 0.f) {
+          int better = 0;
+          for (int c = 0; c < near; ++c) {
+            const double x = __shfl_sync(0xffffffffu, v, c);
+            better += x > v || (x == v && c < lane);
+          }
+          const uint32_t stay = __ballot_sync(0xffffffffu, lane < near && better < need);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (i >= places) break;
-      const float f = unkey32(key[i]);
-      const bool near = key[i] != 0 && !(f > t + 2.f * bound) && !(f < t - 2.f * bound);
-      uint32_t m = __ballot_sync(0xffffffffu, near);
-      while (m) {
-        const int l = __ffs(m) - 1;
-        m &= m - 1;
-        const double v = exact_score<D>(a, qs, head, i * 32 + l);
-        if (lane == l) exact[i * 32 + l] = v;
+          for (int i = 0; i < VPL; ++i)
+            if (i < places && key[i] != 0) {
+              if (key[i] - 2u < 32u) key[i] = (stay >> (key[i] - 2u)) & 1u;
+              else if (!score_above(unkey32(key[i]), t, bound)) key[i] = 0;
+            }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (i < places && key[i] > 1u && !score_above(unkey32(key[i]), t, bound)) key[i] = 0;
+        }
+      } else {
+        // many (a flat row): exact values in scratch, each lane its own
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          if (i >= places) break;
+          const bool is = key[i] != 0 && score_near(unkey32(key[i]), t, bound);
+          for (uint32_t m = __ballot_sync(0xffffffffu, is); m; m &= m - 1) {
+            const int l = __ffs(m) - 1;
+            const double x = exact_score<D>(a, qs, head, i * 32 + l);
+            if (lane == l) exact[i * 32 + l] = x;
+          }
+          if (is) key[i] = 1;
+          else if (key[i] != 0 && !score_above(unkey32(key[i]), t, bound)) key[i] = 0;
+        }
+        uint64_t cut64 = 0;
+        for (int b = 63; b >= 0; --b) {
+          const uint64_t trial = cut64 | (1ull << b);
+          int c = 0;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (i < places && key[i] == 1) c += key64(exact[i * 32 + lane]) >= trial;
+          c = __reduce_add_sync(0xffffffffu, c);
+          if (c >= need) cut64 = trial;
+        }
+        int above = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (i < places && key[i] == 1) above += key64(exact[i * 32 + lane]) > cut64;
+        int ties = need - __reduce_add_sync(0xffffffffu, above);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          if (i >= places) break;
+          const uint64_t x = key[i] == 1 ? key64(exact[i * 32 + lane]) : 0ull;
+          const bool tie = key[i] == 1 && x == cut64;
+          const uint32_t m = __ballot_sync(0xffffffffu, tie);
+          if (tie) key[i] = __popc(m & ((1u << lane) - 1)) < ties ? 1u : 0u;
+          else if (key[i] == 1 && x < cut64) key[i] = 0;
+          ties -= min(ties, __popc(m));
+        }
       }
-      if (near) key[i] = 1;                                        // marks a near one
-      else if (key[i] != 0 && !(f > t + 2.f * bound)) key[i] = 0;  // out
     }
-    // each lane reads back only what it wrote itself
-    for (int bit = 63; bit >= 0; --bit) {
-      const uint64_t trial = cut64 | (1ull << bit);
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i < places && key[i] == 1) c += key64(exact[i * 32 + lane]) >= trial;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (c >= need) cut64 = trial;
-    }
-    int above = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i < places && key[i] == 1) above += key64(exact[i * 32 + lane]) > cut64;
-    ties = need - __reduce_add_sync(0xffffffffu, above);
   }
   int at = 0;
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     if (i >= places) break;
     const int j = i * 32 + lane;
-    bool keep = j < r.may && r.forced(j);
-    bool tie = false;
-    if (border && key[i] == 1) {
-      const uint64_t v = key64(exact[j]);
-      keep = v > cut64;
-      tie = v == cut64;
-    } else if (key[i] != 0) {
-      keep = border || key[i] >= low;
-    }
-    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
-    if (tie) keep = __popc(tied & ((1u << lane) - 1)) < ties;
-    ties -= min(ties, __popc(tied));
+    const bool keep = (j < r.may && r.forced(j)) || (border ? key[i] != 0 : key[i] >= low);
     const uint32_t m = __ballot_sync(0xffffffffu, keep);
     if (keep) out[at + __popc(m & ((1u << lane) - 1))] = j;
     at += __popc(m);
@@ -243,8 +318,9 @@ __device__ void select_row(const SelectArgs &a, const float *s, double *exact, f
 // into bf16 high and low parts: each low part's rounding and the omitted lo lo
 // are at most 2^-16 of a product, the roundings of the fp32 sums (24 matrix
 // steps) less than 2^-17, so the error is below 2^-14 |q| |mean| (norms of the
-// head-wise absolute sum and of the block's mean).  The CTA's scores stay in
-// its own scratch rows (read back from L2 by the same CTA).
+// head-wise absolute sum and of the block's mean).  The queries' parts stay in
+// registers, the means' stream through two buffers; the scores go to the CTA's
+// own scratch rows (read back from L2) and a warp per row picks.
 constexpr int kSelTile = 64, kSelThreads = 128;
 constexpr float kSelSplitError = 1.f / 16384.f;
 
@@ -262,16 +338,51 @@ __device__ __forceinline__ void split8(const float (&f)[8], uint4 &hi, uint4 &lo
   lo = pack8(l);
 }
 
+// The means' two parts, zeros behind the last block, and each tile's largest
+// norm: one CTA per tile of 64 blocks.
+template <int D>
+__global__ void __launch_bounds__(256) block_select_split_kernel(const SelectArgs a, int tiles) {
+  __shared__ uint32_t mn;
+  const int head = blockIdx.x / tiles, tile = blockIdx.x % tiles;
+  if (threadIdx.x == 0) mn = 0;
+  __syncthreads();
+  constexpr int COLS = D / 8;
+  for (int i = threadIdx.x; i < kSelTile * COLS; i += 256) {
+    const int r = i / COLS, c = i % COLS, j = tile * kSelTile + r;
+    float f[8], nn = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = 0.f;
+    if (j < a.nblk) {
+      const float4 *src = reinterpret_cast<const float4 *>(a.mean + (static_cast<int64_t>(head) * a.nblk + j) * D + 8 * c);
+      const float4 x = __ldg(src), y = __ldg(src + 1);
+      f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+      f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) nn += f[e] * f[e];
+    nn = norm_part(nn, f);
+    uint4 hi, lo;
+    split8(f, hi, lo);
+    const int64_t at = (static_cast<int64_t>(head) * tiles * kSelTile + j) * D + 8 * c;
+    *reinterpret_cast<uint4 *>(a.mean_hi + at) = hi;
+    *reinterpret_cast<uint4 *>(a.mean_lo + at) = lo;
+#pragma unroll
+    for (int o = COLS / 2; o > 0; o >>= 1) nn += __shfl_xor_sync(0xffffffffu, nn, o);
+    // a NaN or infinite mean makes every comparison an exact one; values >= 0 order like integers
+    if (c == 0) atomicMax(&mn, nn <= 3.4e38f ? __float_as_uint(nn) : 0x7F800000u);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) a.tile_norm[blockIdx.x] = __uint_as_float(mn);
+}
+
 template <int D, int VPL>
-__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kSelThreads, VPL <= 32 ? 3 : 2) block_select_kernel(const SelectArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float qn[kSelTile];       // |q| of every row
-  __shared__ uint32_t mn;              // largest |mean|^2, as bits (values >= 0 order like integers)
   constexpr int TILE = kSelTile * D * 2, COLS = D / 8;
   const uint32_t base = smem_u32(smem);
-  const uint32_t q_hi = base, q_lo = base + TILE, m_hi = base + 2 * TILE, m_lo = base + 3 * TILE;
-  const int warp = warp_id(), lane = lane_id();
-  const int qtiles = (a.Nq + kSelTile - 1) / kSelTile;
+  const int warp = warp_id();
+  const int qtiles = (a.Nq + kSelTile - 1) / kSelTile, tiles = (a.nblk + kSelTile - 1) / kSelTile;
   const int64_t items = static_cast<int64_t>(qtiles) * a.BHk;
   float *scores = a.scores + static_cast<int64_t>(blockIdx.x) * kSelTile * a.nblk;
   double *exact = a.exact + (static_cast<int64_t>(blockIdx.x) * (kSelThreads / 32) + warp) * a.nblk;
@@ -281,9 +392,22 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
     const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
     const int last = min(n0 + kSelTile, a.Nq) - 1;
     const int most = select_range(a, len, last).may;
-    if (threadIdx.x == 0) mn = 0;
-    __syncthreads();
-    // queries: sum over heads, split
+    const __nv_bfloat16 *hi = a.mean_hi + static_cast<int64_t>(head) * tiles * kSelTile * D;
+    const __nv_bfloat16 *lo = a.mean_lo + static_cast<int64_t>(head) * tiles * kSelTile * D;
+    auto fetch = [&](int t) {          // tile t of the means' parts
+      if (t * kSelTile < most) {
+        const uint32_t dst = base + static_cast<uint32_t>(t & 1) * 2 * TILE;
+        for (int i = threadIdx.x; i < kSelTile * COLS; i += kSelThreads) {
+          const int r = i / COLS, c = i % COLS;
+          const int64_t at = (static_cast<int64_t>(t) * kSelTile + r) * D + 8 * c;
+          cp_async16(dst + tile_at<D>(r, c), hi + at, 16);
+          cp_async16(dst + TILE + tile_at<D>(r, c), lo + at, 16);
+        }
+      }
+      cp_async_commit();
+    };
+    fetch(0);
+    // queries: sum over heads, split, by way of the second buffer into registers
     for (int i = threadIdx.x; i < kSelTile * COLS; i += kSelThreads) {
       const int r = i / COLS, c = i % COLS;
       float f[8], ab = 0.f;
@@ -305,40 +429,32 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) ab += z[e] * z[e];
+        ab = norm_part(ab, z);
       }
-      uint4 hi, lo;
-      split8(f, hi, lo);
-      *reinterpret_cast<uint4 *>(smem + tile_at<D>(r, c)) = hi;
-      *reinterpret_cast<uint4 *>(smem + TILE + tile_at<D>(r, c)) = lo;
+      uint4 h, l;
+      split8(f, h, l);
+      *reinterpret_cast<uint4 *>(smem + 2 * TILE + tile_at<D>(r, c)) = h;
+      *reinterpret_cast<uint4 *>(smem + 3 * TILE + tile_at<D>(r, c)) = l;
 #pragma unroll
       for (int o = COLS / 2; o > 0; o >>= 1) ab += __shfl_xor_sync(0xffffffffu, ab, o);
       if (c == 0) qn[r] = sqrtf(ab);
     }
-    for (int j0 = 0; j0 < most; j0 += kSelTile) {
-      for (int i = threadIdx.x; i < kSelTile * COLS; i += kSelThreads) {
-        const int r = i / COLS, c = i % COLS;
-        float f[8], nn = 0.f;
+    __syncthreads();
+    uint32_t ah[D / 16][4], al[D / 16][4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = 0.f;
-        if (j0 + r < most) {
-          const float4 *src = reinterpret_cast<const float4 *>(
-              a.mean + (static_cast<int64_t>(head) * a.nblk + j0 + r) * D + 8 * c);
-          const float4 x = __ldg(src), y = __ldg(src + 1);
-          f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-          f[4] = y.x; f[5] = y.y; f[6] = y.z; f[7] = y.w;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) nn += f[e] * f[e];
-        uint4 hi, lo;
-        split8(f, hi, lo);
-        *reinterpret_cast<uint4 *>(smem + 2 * TILE + tile_at<D>(r, c)) = hi;
-        *reinterpret_cast<uint4 *>(smem + 3 * TILE + tile_at<D>(r, c)) = lo;
-#pragma unroll
-        for (int o = COLS / 2; o > 0; o >>= 1) nn += __shfl_xor_sync(0xffffffffu, nn, o);
-        // a NaN or infinite mean makes every comparison an exact one
-        if (c == 0) atomicMax(&mn, nn <= 3.4e38f ? __float_as_uint(nn) : 0x7F800000u);
-      }
+    for (int ks = 0; ks < D / 16; ++ks) {
+      ldsm_x4(ldsm_a<D>(base + 2 * TILE, 16 * warp, ks), ah[ks]);
+      ldsm_x4(ldsm_a<D>(base + 3 * TILE, 16 * warp, ks), al[ks]);
+    }
+    __syncthreads();
+    float norm = 0.f;
+    for (int tile = 0; tile * kSelTile < most; ++tile) {
+      const int j0 = tile * kSelTile;
+      norm = fmaxf(norm, a.tile_norm[head * tiles + tile]);
+      fetch(tile + 1);
+      cp_async_wait<1>();
       __syncthreads();
+      const uint32_t m_hi = base + static_cast<uint32_t>(tile & 1) * 2 * TILE, m_lo = m_hi + TILE;
       float acc[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -346,20 +462,17 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
         for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t ah[4], al[4];
-        ldsm_x4(ldsm_a<D>(q_hi, 16 * warp, ks), ah);
-        ldsm_x4(ldsm_a<D>(q_lo, 16 * warp, ks), al);
 #pragma unroll
         for (int t = 0; t < 8; t += 2) {
           uint32_t bh[4], bl[4];
           ldsm_x4(ldsm_b<D>(m_hi, 8 * t, ks), bh);
           ldsm_x4(ldsm_b<D>(m_lo, 8 * t, ks), bl);
-          mma_bf16(acc[t], al, bh[0], bh[1]);
-          mma_bf16(acc[t + 1], al, bh[2], bh[3]);
-          mma_bf16(acc[t], ah, bl[0], bl[1]);
-          mma_bf16(acc[t + 1], ah, bl[2], bl[3]);
-          mma_bf16(acc[t], ah, bh[0], bh[1]);
-          mma_bf16(acc[t + 1], ah, bh[2], bh[3]);
+          mma_bf16(acc[t], al[ks], bh[0], bh[1]);
+          mma_bf16(acc[t + 1], al[ks], bh[2], bh[3]);
+          mma_bf16(acc[t], ah[ks], bl[0], bl[1]);
+          mma_bf16(acc[t + 1], ah[ks], bl[2], bl[3]);
+          mma_bf16(acc[t], ah[ks], bh[0], bh[1]);
+          mma_bf16(acc[t + 1], ah[ks], bh[2], bh[3]);
         }
       }
       const int r0 = 16 * warp + frag_row();
@@ -372,10 +485,10 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
         }
       __syncthreads();
     }
-    __syncthreads();
-    const float mnorm = sqrtf(__uint_as_float(mn));
+    // a warp reads only the rows that it wrote
+    norm = sqrtf(norm);
     for (int r = 16 * warp; r < 16 * warp + 16 && n0 + r < a.Nq; ++r) {
-      float bound = kSelSplitError * qn[r] * mnorm;
+      float bound = kSelSplitError * qn[r] * norm;
       if (!(bound <= 3.4e38f)) bound = INFINITY;
       select_row<D, VPL>(a, scores + static_cast<int64_t>(r) * a.nblk, exact, bound, head, n0 + r,
                          select_range(a, len, n0 + r));
@@ -387,22 +500,45 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const SelectA
 
 // Few queries: one CTA per (key head, query).  8 lanes (D = 64: 4) form one
 // score in fp32; 16 products, two levels of sums: error below 2^-18 |q| |mean|.
-// HBM bound: reads the means once.
+// HBM bound: reads the means once.  All threads search the border together.
 constexpr int kSelDecodeThreads = 512;
 constexpr float kSelDotError = 1.f / 262144.f;
+constexpr int kSelDecodePlaces = kMaxBlocks / kSelDecodeThreads;
 
-template <int D, int VPL>
+// Shared memory: exact scores, their blocks, approximate scores, kept blocks.
+__host__ __device__ inline size_t select_decode_smem(int nblk) {
+  return static_cast<size_t>(nblk) * 16 + (nblk + 31) / 32 * 4 + 4;
+}
+
+// Sum over the CTA; `turn` alternates between two rows of warp sums.
+__device__ __forceinline__ int cta_sum(int v, int (&part)[2][kSelDecodeThreads / 32], int turn) {
+  v = __reduce_add_sync(0xffffffffu, v);
+  if (lane_id() == 0) part[turn & 1][warp_id()] = v;
+  __syncthreads();
+  const int x = lane_id() < kSelDecodeThreads / 32 ? part[turn & 1][lane_id()] : 0;
+  return __reduce_add_sync(0xffffffffu, x);
+}
+
+template <int D>
 __global__ void __launch_bounds__(kSelDecodeThreads) block_select_decode_kernel(const SelectArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   double *exact = reinterpret_cast<double *>(smem);               // [nblk]
   float *scores = reinterpret_cast<float *>(exact + a.nblk);      // [nblk]
-  __shared__ uint32_t mn;
-  constexpr int GT = D / 16;
+  int *who = reinterpret_cast<int *>(scores + a.nblk);            // [nblk]
+  uint32_t *kept = reinterpret_cast<uint32_t *>(who + a.nblk);    // bit set of the list
+  __shared__ uint32_t mn, top, least;
+  __shared__ int part[2][kSelDecodeThreads / 32], nears;
+  constexpr int GT = D / 16, WARPS = kSelDecodeThreads / 32;
   const int head = blockIdx.x / a.Nq, n = blockIdx.x % a.Nq;
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const SelectRange r = select_range(a, len, n);
   const int c = threadIdx.x % GT;
-  if (threadIdx.x == 0) mn = 0;
+  if (threadIdx.x == 0) {
+    mn = top = 0;
+    least = 0xFFFFFFFFu;
+    nears = 0;
+  }
+  for (int i = threadIdx.x; i < (a.nblk + 31) / 32; i += kSelDecodeThreads) kept[i] = 0;
   float qs[16], qa = 0.f;
   {
     float z[16];
@@ -424,37 +560,138 @@ __global__ void __launch_bounds__(kSelDecodeThreads) block_select_decode_kernel(
     }
 #pragma unroll
     for (int e = 0; e < 16; ++e) qa += z[e] * z[e];
-    qa = row_sum<D>(qa);
+    qa = row_sum<D>(norm_part(qa, z));
   }
   __syncthreads();
   uint32_t biggest = 0;
-  const int rounds = (r.may + kSelDecodeThreads / GT - 1) / (kSelDecodeThreads / GT);
-#pragma unroll 2
-  for (int i = 0; i < rounds; ++i) {
-    const int j = i * (kSelDecodeThreads / GT) + threadIdx.x / GT;
-    float s = 0.f, nn = 0.f;
-    if (j < r.may) {
+  constexpr int PER = kSelDecodeThreads / GT, U = 4;              // blocks of a round, rounds in flight
+  for (int j0 = 0; j0 < r.may; j0 += PER * U) {
+    float4 v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * PER + threadIdx.x / GT;
       const float4 *src = reinterpret_cast<const float4 *>(a.mean + (static_cast<int64_t>(head) * a.nblk + j) * D);
-      const float4 v[4] = {__ldg(src + 2 * c), __ldg(src + 2 * c + 1), __ldg(src + 2 * GT + 2 * c),
-                           __ldg(src + 2 * GT + 2 * c + 1)};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        v[u][e] = j < r.may ? __ldg(src + (e < 2 ? 2 * c + e : 2 * GT + 2 * c + e - 2)) : make_float4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u * PER + threadIdx.x / GT;
+      float s = 0.f, nn = 0.f;
+      bool none = true;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s += v[e].x * qs[4 * e] + v[e].y * qs[4 * e + 1] + v[e].z * qs[4 * e + 2] + v[e].w * qs[4 * e + 3];
-        nn += v[e].x * v[e].x + v[e].y * v[e].y + v[e].z * v[e].z + v[e].w * v[e].w;
+        none = none && v[u][e].x == 0.f && v[u][e].y == 0.f && v[u][e].z == 0.f && v[u][e].w == 0.f;
+        s += v[u][e].x * qs[4 * e] + v[u][e].y * qs[4 * e + 1] + v[u][e].z * qs[4 * e + 2] + v[u][e].w * qs[4 * e + 3];
+        nn += v[u][e].x * v[u][e].x + v[u][e].y * v[u][e].y + v[u][e].z * v[u][e].z + v[u][e].w * v[u][e].w;
       }
+      s = row_sum<D>(s);
+      nn = row_sum<D>(none ? 0.f : nn < kNormFloor ? kNormFloor : nn);
+      if (j < r.may && c == 0) scores[j] = s;
+      biggest = max(biggest, nn <= 3.4e38f ? __float_as_uint(nn) : 0x7F800000u);
     }
-    s = row_sum<D>(s);
-    nn = row_sum<D>(nn);
-    if (j < r.may && c == 0) scores[j] = s;
-    biggest = max(biggest, nn <= 3.4e38f ? __float_as_uint(nn) : 0x7F800000u);
   }
   biggest = __reduce_max_sync(0xffffffffu, biggest);
   if (lane_id() == 0) atomicMax(&mn, biggest);
   __syncthreads();
+  float bound = kSelDotError * sqrtf(qa) * sqrtf(__uint_as_float(mn));
+  if (!(bound <= 3.4e38f)) bound = INFINITY;
+
+  // block i * 512 + thread, place i
+  const int forced = r.num_forced();
+  int need = a.topk - forced;
+  uint32_t key[kSelDecodePlaces], mine = 0;
+#pragma unroll
+  for (int i = 0; i < kSelDecodePlaces; ++i) {
+    const int j = i * kSelDecodeThreads + threadIdx.x;
+    key[i] = (j < r.may && !r.forced(j)) ? key32(scores[j]) : 0u;
+    mine = max(mine, key[i]);
+    if (j < r.may && r.forced(j)) atomicOr(&kept[j >> 5], 1u << (j & 31));
+  }
+  if (r.may - forced <= need) {
+#pragma unroll
+    for (int i = 0; i < kSelDecodePlaces; ++i) {
+      const int j = i * kSelDecodeThreads + threadIdx.x;
+      if (key[i] != 0) atomicOr(&kept[j >> 5], 1u << (j & 31));
+    }
+  } else if (need > 0) {
+    mine = __reduce_max_sync(0xffffffffu, mine);
+    if (lane_id() == 0) atomicMax(&top, mine);
+    __syncthreads();
+    int turn = 0;
+    uint32_t cut = 0;
+    for (int bit = 31 - __clz(top); bit >= 0; --bit) {
+      const uint32_t trial = cut | (1u << bit);
+      int x = 0;
+#pragma unroll
+      for (int i = 0; i < kSelDecodePlaces; ++i) x += key[i] >= trial;
+      x = cta_sum(x, part, turn++);
+      if (x >= need) cut = trial;
+      if (x == need) break;
+    }
+    uint32_t l = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kSelDecodePlaces; ++i)
+      if (key[i] >= cut && key[i] != 0) l = min(l, key[i]);
+    l = __reduce_min_sync(0xffffffffu, l);
+    if (lane_id() == 0) atomicMin(&least, l);
+    __syncthreads();
+    const float t = unkey32(least);
+    int sure = 0;
+#pragma unroll
+    for (int i = 0; i < kSelDecodePlaces; ++i) {
+      const int j = i * kSelDecodeThreads + threadIdx.x;
+      if (key[i] == 0) continue;
+      const float f = unkey32(key[i]);
+      if (score_above(f, t, bound)) {
+        ++sure;
+        atomicOr(&kept[j >> 5], 1u << (j & 31));
+      } else if (score_near(f, t, bound)) {
+        who[atomicAdd(&nears, 1)] = j;
+      }
+    }
+    need -= cta_sum(sure, part, turn);
+    const int near = nears;
+    if (near > need) {
+      // exact scores, then each one's rank (better score, or lower block)
+      double q64[D / 32];
+      exact_query<D>(a, q64, head, n);
+      for (int i = warp_id(); i < near; i += WARPS) {
+        double x = exact_score<D>(a, q64, head, who[i]);
+        if (x != x) x = -INFINITY;
+        if (lane_id() == 0) exact[i] = x;
+      }
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < near; i += kSelDecodeThreads) {
+      const int j = who[i];
+      int better = 0;
+      if (near > need)
+        for (int o = 0; o < near; ++o) better += exact[o] > exact[i] || (exact[o] == exact[i] && who[o] < j);
+      if (near <= need || better < need) atomicOr(&kept[j >> 5], 1u << (j & 31));
+    }
+  }
+  __syncthreads();
   if (warp_id() == 0) {
-    float bound = kSelDotError * sqrtf(qa) * sqrtf(__uint_as_float(mn));
-    if (!(bound <= 3.4e38f)) bound = INFINITY;
-    select_row<D, VPL>(a, scores, exact, bound, head, n, r);
+    int32_t *out = a.sel + (static_cast<int64_t>(head) * a.Nq + n) * a.topk;
+    const int words = (a.nblk + 31) / 32;
+    int at = 0;
+    for (int w0 = 0; w0 < words; w0 += 32) {
+      const int w = w0 + lane_id();
+      uint32_t u = w < words ? kept[w] : 0u;
+      int pre = __popc(u);
+      const int own = pre;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, pre, o);
+        if (static_cast<int>(lane_id()) >= o) pre += x;
+      }
+      int p = at + pre - own;
+      for (; u; u &= u - 1) out[p++] = w * 32 + __ffs(u) - 1;
+      at += __shfl_sync(0xffffffffu, pre, 31);
+    }
+    for (int i = at + lane_id(); i < a.topk; i += 32) out[i] = -1;
   }
 }
 

@@ -995,6 +995,19 @@ int select_ctas(int BHk, int Nq) {
   return static_cast<int>(items < most ? items : most);
 }
 
+SelectArgs carve_select(void *ws, int BHk, int Nq, int nblk, int D, size_t *bytes) {
+  Carve c{static_cast<uint8_t *>(ws)};
+  SelectArgs a{};
+  const size_t tiles = (nblk + kSelTile - 1) / kSelTile, ctas = select_ctas(BHk, Nq);
+  a.exact = c.take<double>(ctas * (kSelThreads / 32) * nblk);
+  a.scores = c.take<float>(ctas * kSelTile * nblk);
+  a.mean_hi = c.take<__nv_bfloat16>(BHk * tiles * kSelTile * D);
+  a.mean_lo = c.take<__nv_bfloat16>(BHk * tiles * kSelTile * D);
+  a.tile_norm = c.take<float>(BHk * tiles);
+  *bytes = c.used;
+  return a;
+}
+
 struct BlockAttnPlan {
   bool few;
   int tokens, tiles, splits;
@@ -1093,12 +1106,12 @@ svg_status svg_block_mean(const void *k, int BHk, int B, int Nk, int D, int bloc
   return launch_status("block_mean_kernel");
 }
 
-size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int block) {
-  if (BHk <= 0 || Nq <= 0 || Nk <= 0 || block <= 0 || !sizes_ok(BHk, Nq)) return 0;
+size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int D, int block) {
+  if (BHk <= 0 || Nq <= 0 || Nk <= 0 || D <= 0 || block <= 0 || !sizes_ok(BHk, Nq) || !sizes_ok(BHk, Nk)) return 0;
   if (select_few(Nq)) return 0;
-  const size_t nblk = (static_cast<size_t>(Nk) + block - 1) / block;
-  return align256(static_cast<size_t>(select_ctas(BHk, Nq)) * nblk *
-                  (kSelTile * sizeof(float) + kSelThreads / 32 * sizeof(double)));
+  size_t bytes = 0;
+  carve_select(nullptr, BHk, Nq, (Nk + block - 1) / block, D, &bytes);
+  return bytes;
 }
 
 svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, int B, int Nq, int Nk, int D, int block,
@@ -1112,10 +1125,12 @@ svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, 
   if (st != SVG_OK) return st;
   if (topk > kMaxBlockTopk) return SVG_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(mean, 16) || !aligned(ws, 256)) return SVG_ERR_INVALID_ARG;
-  const size_t need = svg_block_select_workspace_size(BHk, Nq, Nk, block);
+  const size_t need = svg_block_select_workspace_size(BHk, Nq, Nk, D, block);
   if (need > 0 && !ws) return SVG_ERR_INVALID_ARG;
   if (ws_bytes < need) return SVG_ERR_WORKSPACE;
-  SelectArgs a{};
+  const bool few = select_few(Nq);
+  size_t used = 0;
+  SelectArgs a = few ? SelectArgs{} : carve_select(ws, BHk, Nq, nblk, D, &used);
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.mean = mean;
   a.kv_len = kv_len;
@@ -1132,31 +1147,35 @@ svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, 
   a.local = local;
   a.causal = causal;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool few = select_few(Nq);
-  const int ctas = few ? BHk * Nq : select_ctas(BHk, Nq);
-  if (!few) {
-    a.exact = static_cast<double *>(ws);
-    a.scores = reinterpret_cast<float *>(a.exact + static_cast<size_t>(ctas) * (kSelThreads / 32) * nblk);
+  if (few) {
+    auto one = [&](auto kernel) {
+      const size_t smem = select_decode_smem(nblk);
+      if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
+      kernel<<<BHk * Nq, kSelDecodeThreads, smem, s>>>(a);
+      return launch_status("block_select_decode_kernel");
+    };
+    return D == 128 ? one(block_select_decode_kernel<128>) : one(block_select_decode_kernel<64>);
   }
-  auto go = [&](auto one, auto many, size_t tile_bytes) {
-    if (few) {
-      const size_t smem = static_cast<size_t>(nblk) * (sizeof(double) + sizeof(float));
-      if (!set_smem(one, smem)) return SVG_ERR_CUDA;
-      one<<<ctas, kSelDecodeThreads, smem, s>>>(a);
-    } else {
-      if (!set_smem(many, tile_bytes)) return SVG_ERR_CUDA;
-      many<<<ctas, kSelThreads, tile_bytes, s>>>(a);
-    }
+  const int tiles = (nblk + kSelTile - 1) / kSelTile;
+  auto many = [&](auto split, auto kernel, size_t smem) {
+    if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
+    split<<<BHk * tiles, 256, 0, s>>>(a, tiles);
+    kernel<<<select_ctas(BHk, Nq), kSelThreads, smem, s>>>(a);
     return launch_status("block_select_kernel");
   };
+  // places of a lane: a row's keys stay in registers
   if (D == 128) {
-    if (nblk <= 256) return go(block_select_decode_kernel<128, 8>, block_select_kernel<128, 8>, select_smem<128>());
-    if (nblk <= 1024) return go(block_select_decode_kernel<128, 32>, block_select_kernel<128, 32>, select_smem<128>());
-    return go(block_select_decode_kernel<128, 128>, block_select_kernel<128, 128>, select_smem<128>());
+    auto split = block_select_split_kernel<128>;
+    if (nblk <= 128) return many(split, block_select_kernel<128, 4>, select_smem<128>());
+    if (nblk <= 512) return many(split, block_select_kernel<128, 16>, select_smem<128>());
+    if (nblk <= 1024) return many(split, block_select_kernel<128, 32>, select_smem<128>());
+    return many(split, block_select_kernel<128, 128>, select_smem<128>());
   }
-  if (nblk <= 256) return go(block_select_decode_kernel<64, 8>, block_select_kernel<64, 8>, select_smem<64>());
-  if (nblk <= 1024) return go(block_select_decode_kernel<64, 32>, block_select_kernel<64, 32>, select_smem<64>());
-  return go(block_select_decode_kernel<64, 128>, block_select_kernel<64, 128>, select_smem<64>());
+  auto split = block_select_split_kernel<64>;
+  if (nblk <= 128) return many(split, block_select_kernel<64, 4>, select_smem<64>());
+  if (nblk <= 512) return many(split, block_select_kernel<64, 16>, select_smem<64>());
+  if (nblk <= 1024) return many(split, block_select_kernel<64, 32>, select_smem<64>());
+  return many(split, block_select_kernel<64, 128>, select_smem<64>());
 }
 
 size_t svg_block_attn_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block) {

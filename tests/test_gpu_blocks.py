@@ -267,6 +267,22 @@ def test_selection_of_degenerate_scores(Nq):
     assert np.array_equal(sel.cpu().numpy(), want), np.argwhere(sel.cpu().numpy() != want)[:5]
 
 
+@pytest.mark.parametrize("Nq", [1, 66])
+def test_selection_of_flat_and_tiny_scores(Nq):
+    """More near candidates than a warp has lanes, and norms whose squares underflow."""
+    q, Nk, D = bf(54, 3, Nq, 64), 6400, 64
+    q[2] = (q[2].double() * 1e-25).to(BF)
+    mean = torch.randn(3, 100, D, generator=torch.Generator().manual_seed(55)).cuda()
+    noise = torch.randn(100, D, generator=torch.Generator().manual_seed(56)).cuda()
+    mean[0] = mean[0, :1] * (1 + noise * 2.0 ** -23)          # all within the approximate scores' error
+    mean[1] = mean[1, :1]
+    mean[1, 50:] = mean[1, 50:] * (1 + 2.0 ** -22)
+    mean[2] = mean[2] * 1e-15
+    sel = svg.block_select(q, mean, 64, 9, Nk, 1, 1, True)
+    want = bo.select_blocks(f64(q), f64(mean), 64, 9, 1, 1, True, [Nk] * 3)
+    assert np.array_equal(sel.cpu().numpy(), want), np.argwhere(sel.cpu().numpy() != want)[:5]
+
+
 # ----------------------------------------------------------------------- attention
 ATTN = [  # B, Hq, Hk, Nq, Nk, D, block, topk, causal, lens
     (1, 1, 1, 1, 1, 64, 64, 1, True, None),
