@@ -71,8 +71,10 @@ struct SelectArgs {
   // many queries only (workspace):
   __nv_bfloat16 *mean_hi, *mean_lo;    // [BHk, nblk up to whole tiles, D]: the means' bf16 parts
   float *tile_norm;                    // [BHk, tiles] largest |mean|^2 of a tile
-  float *scores;                       // per CTA [64][nblk]
-  double *exact;                       // per warp [nblk]
+  float *scores;                       // [items of a part][64][nblk up to whole tiles]
+  float *bounds;                       // [items of a part][64] error bound of a row's scores
+  double *exact;                       // per warp of the picking kernel [nblk]
+  int item0, items;                    // the part's first item, and how many
   int BHk, G, heads_per_seq, Nq, Nk, nblk, block, topk, sink, local, causal;
 };
 
@@ -109,25 +111,48 @@ __device__ __forceinline__ SelectRange select_range(const SelectArgs &a, int len
   return r;
 }
 
-// Exact score of block j from the lane's summed query channels: every lane returns it.
+// Exact score of block j: the lane's share, from its channels of the summed
+// query, and the whole (every lane returns it).
 template <int D>
-__device__ __forceinline__ double exact_score(const SelectArgs &a, const double (&qs)[D / 32], int head, int j) {
-  const float *m = a.mean + (static_cast<int64_t>(head) * a.nblk + j) * D + lane_id() * (D / 32);
+__device__ __forceinline__ double exact_part(const SelectArgs &a, const double (&qs)[D / 32], int head, int j) {
+  const float2 *m = reinterpret_cast<const float2 *>(a.mean + (static_cast<int64_t>(head) * a.nblk + j) * D +
+                                                     lane_id() * (D / 32));
   double s = 0.0;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) s += qs[i] * static_cast<double>(m[i]);
+  for (int i = 0; i < D / 64; ++i) {
+    const float2 v = __ldg(m + i);
+    s += qs[2 * i] * static_cast<double>(v.x) + qs[2 * i + 1] * static_cast<double>(v.y);
+  }
+  return s;
+}
+template <int D>
+__device__ __forceinline__ double exact_score(const SelectArgs &a, const double (&qs)[D / 32], int head, int j) {
+  double s = exact_part<D>(a, qs, head, j);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 template <int D>
 __device__ __forceinline__ void exact_query(const SelectArgs &a, double (&qs)[D / 32], int head, int n) {
+  const __nv_bfloat16 *src = a.q + (static_cast<int64_t>(head) * a.G * a.Nq + n) * D + lane_id() * (D / 32);
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    qs[i] = 0.0;
-    for (int g = 0; g < a.G; ++g)
-      qs[i] += static_cast<double>(__bfloat162float(
-          a.q[((static_cast<int64_t>(head) * a.G + g) * a.Nq + n) * D + lane_id() * (D / 32) + i]));
+  for (int i = 0; i < D / 32; ++i) qs[i] = 0.0;
+  for (int g0 = 0; g0 < a.G; g0 += 4) {             // 4 loads in flight
+    uint32_t x[4][D / 64];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        x[g][i] = 0;
+        if (g0 + g < a.G) x[g][i] = *reinterpret_cast<const uint32_t *>(src + static_cast<int64_t>(g0 + g) * a.Nq * D + 2 * i);
+      }
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        qs[2 * i] += static_cast<double>(__uint_as_float(x[g][i] << 16));
+        qs[2 * i + 1] += static_cast<double>(__uint_as_float(x[g][i] & 0xFFFF0000u));
+      }
   }
 }
 
@@ -151,161 +176,240 @@ __device__ __forceinline__ bool score_near(float f, float t, float bound) {
   return !score_above(f, t, bound) && !(f < t - 2.f * bound);
 }
 
-// One warp writes one query's list.  s: approximate scores of the blocks
-// [0, r.may); bound: their largest error; exact: scratch of nblk doubles.
-// Block j belongs to lane j % 32, place j / 32.
+// Exact scores of the `count` <= 32 near blocks at `near`: bit c of the result
+// says that the c-th is among the `need` best (better score, or lower block).
+template <int D>
+__device__ __noinline__ uint32_t rank_near(const SelectArgs &a, const int *near, int count, int need, int head, int n) {
+  const int lane = lane_id();
+  double qs[D / 32], v = 0.0;
+  exact_query<D>(a, qs, head, n);
+  for (int c0 = 0; c0 < count; c0 += 4) {           // 4 at a time, for their latency
+    double x[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] = exact_part<D>(a, qs, head, near[min(c0 + c, count - 1)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], o);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (lane == c0 + c) v = x[c] != x[c] ? -INFINITY : x[c];
+  }
+  int better = 0;
+  for (int c = 0; c < count; ++c) {
+    const double x = __shfl_sync(0xffffffffu, v, c);
+    better += x > v || (x == v && c < lane);
+  }
+  return __ballot_sync(0xffffffffu, lane < count && better < need);
+}
+
+// One warp writes one query's list, in two ways.  s: approximate scores of the
+// blocks [0, r.may); bound: their largest error.  Block j belongs to lane
+// j % 32, place j / 32.
+//
+// The ordinary one keeps the row in registers (VPL places; forced blocks and
+// places without one are NaN, which no comparison takes) and finds the last
+// place's score by bisection, from the largest score down to a lower bound of
+// it: the smallest of the lanes' largest scores while topk <= 32, else the
+// smallest score.  Returns false, with nothing written, for rows that are flat
+// (more than 32 near the border) or hold infinities.
 template <int D, int VPL>
-__device__ void select_row(const SelectArgs &a, const float *s, double *exact, float bound, int head, int n,
-                           const SelectRange &r) {
+__device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, int *near_list, float bound, int head,
+                                           int n, const SelectRange &r) {
+  const uint32_t all = 0xffffffffu;
+  const int lane = lane_id();
+  const uint32_t below = (1u << lane) - 1;
+  int32_t *out = a.sel + (static_cast<int64_t>(head) * a.Nq + n) * a.topk;
+  if (r.may <= a.topk) {                            // every block
+    for (int i = lane; i < a.topk; i += 32) out[i] = i < r.may ? i : -1;
+    return true;
+  }
+  const int need = a.topk - r.num_forced();
+  const float none = __int_as_float(0x7FFFFFFF);
+  float f[VPL], mine = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {                   // no branch between them: all loads in flight
+    f[i] = none;
+    if (i * 32 + lane < r.may) f[i] = s[i * 32 + lane];
+  }
+  // NaN counts as -inf; the places with forced blocks are the first and the last few
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (i * 32 >= r.may) break;
+    f[i] = i * 32 + lane < r.may ? fmaxf(f[i], -INFINITY) : none;
+    if (i * 32 < r.s1 || (i * 32 < r.l1 && i * 32 + 31 >= r.l0))
+      if (r.forced(i * 32 + lane)) f[i] = none;
+    mine = fmaxf(mine, f[i]);
+  }
+  float hi = unkey32(__reduce_max_sync(all, key32(mine)));
+  float lo = unkey32(__reduce_min_sync(all, key32(mine)));
+  if (lo == -INFINITY || need > 32) {               // a lane without a candidate
+    mine = INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) mine = fminf(mine, f[i]);
+    lo = unkey32(__reduce_min_sync(all, key32(mine)));
+  }
+  if (need == 0 || !(hi - lo < 3.0e38f)) return false;
+  auto count = [&](float x) {
+    float c0 = 0.f, c1 = 0.f;                       // a comparison yields 1.0f in one instruction
+#pragma unroll
+    for (int i = 0; i < VPL; i += 2) {
+      if (i % 8 == 0 && i * 32 >= r.may) break;
+      c0 += f[i] >= x ? 1.f : 0.f;
+      c1 += f[i + 1] >= x ? 1.f : 0.f;
+    }
+    return __reduce_add_sync(all, static_cast<int>(c0 + c1));
+  };
+  // at least `need` are not below lo; fewer not below hi, unless lo == hi
+  if (count(hi) >= need) lo = hi;
+  while (lo < hi) {
+    const float mid = lo + 0.5f * (hi - lo);
+    if (!(mid > lo && mid < hi)) break;             // neighbours: equal scores
+    const int c = count(mid);
+    if (c >= need) lo = mid;
+    else hi = mid;
+    if (c == need) break;
+  }
+  // the last place's score, and who is near it
+  float least = INFINITY;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (f[i] >= lo) least = fminf(least, f[i]);
+  const float t = unkey32(__reduce_min_sync(all, key32(least)));
+  const float over = t + 2.f * bound, under = t - 2.f * bound;
+  int both = 0;                                     // near ones above 2^16, above ones below
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (i % 8 == 0 && i * 32 >= r.may) break;
+    both += f[i] > over ? 1 : f[i] >= under ? 1 << 16 : 0;
+  }
+  both = __reduce_add_sync(all, both);
+  const int sure = both & 0xFFFF, nears = both >> 16;
+  uint32_t stay = all;
+  if (nears > need - sure) {
+    if (nears > 32 || !(bound < INFINITY)) return false;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      if (i * 32 >= r.may) break;
+      const bool near = f[i] >= under && !(f[i] > over);
+      const uint32_t m = __ballot_sync(all, near);
+      if (near) near_list[at + __popc(m & below)] = i * 32 + lane;
+      at += __popc(m);
+    }
+    __syncwarp();
+    stay = rank_near<D>(a, near_list, nears, need - sure, head, n);
+  }
+  int seen = 0, at = 0, low = 0;
+  const int l0 = max(r.l0, r.s1);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    if (i * 32 >= r.may) break;
+    const uint32_t cand = __ballot_sync(all, f[i] >= under);
+    if (cand == 0) continue;
+    const uint32_t nm = cand & ~__ballot_sync(all, f[i] > over);
+    const int mine_near = seen + __popc(nm & below);
+    const bool in = ((cand >> lane) & 1u) && (!((nm >> lane) & 1u) || ((stay >> (mine_near & 31)) & 1u));
+    seen += __popc(nm);
+    const uint32_t m = __ballot_sync(all, in);
+    const int j = i * 32 + lane;
+    // before it: forced blocks below it and kept ones
+    if (in) out[at + __popc(m & below) + r.s1 + max(0, min(j, r.l1) - l0)] = j;
+    at += __popc(m);
+    low += __popc(__ballot_sync(all, in && j < l0));
+  }
+  for (int i = lane; i < r.s1; i += 32) out[i] = i;
+  for (int i = l0 + lane; i < r.l1; i += 32) out[low + r.s1 + i - l0] = i;
+  return true;
+}
+
+// The general one reads the scores again for every step; exact: scratch of
+// nblk doubles.
+template <int D>
+__device__ __noinline__ void select_row_any(const SelectArgs &a, const float *s, double *exact, float bound, int head,
+                                            int n, const SelectRange r) {
   const int lane = lane_id();
   int32_t *out = a.sel + (static_cast<int64_t>(head) * a.Nq + n) * a.topk;
   const int places = (r.may + 31) / 32;
-  const int forced = r.num_forced();
-  int need = a.topk - forced;
-  uint32_t key[VPL];
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
+  int need = a.topk - r.num_forced();               // fewer than the others: see select_row
+  auto key = [&](int i) {
     const int j = i * 32 + lane;
-    key[i] = (i < places && j < r.may && !r.forced(j)) ? key32(s[j]) : 0u;
+    return j < r.may && !r.forced(j) ? key32(s[j]) : 0u;
+  };
+  uint32_t cut = 0;
+  for (int bit = 31; bit >= 0 && need > 0; --bit) {
+    const uint32_t trial = cut | (1u << bit);
+    int c = 0;
+    for (int i = 0; i < places; ++i) c += key(i) >= trial;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= need) cut = trial;
+    if (c == need) break;
   }
-  uint32_t low = 1;                    // without a border: keep = key >= low (key 0 never is)
-  bool border = false;
-  float t = 0.f;
-  if (r.may - forced > need) {
-    // The need-th largest key, bit by bit.  While need <= 32, the smallest of
-    // the lanes' largest keys bounds it from below, so the bits that this
-    // bound shares with the largest key are known.
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i < places) mine = max(mine, key[i]);
-    const uint32_t top = __reduce_max_sync(0xffffffffu, mine);
-    const uint32_t floor = need <= 32 ? __reduce_min_sync(0xffffffffu, mine) : 0u;
-    const uint32_t open = top ^ floor;
-    int bit = open ? 31 - __clz(open) : -1;
-    uint32_t cut = bit < 0 ? top : bit == 31 ? 0u : (top >> (bit + 1)) << (bit + 1);
-    for (; bit >= 0; --bit) {
-      const uint32_t trial = cut | (1u << bit);
+  uint32_t least = 0xFFFFFFFFu;
+  for (int i = 0; i < places; ++i) {
+    const uint32_t k = key(i);
+    if (k >= cut && k != 0) least = min(least, k);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  const float t = unkey32(least);
+  int sure = 0, near = 0;
+  for (int i = 0; i < places && need > 0; ++i) {
+    const uint32_t k = key(i);
+    if (k != 0) {
+      sure += score_above(unkey32(k), t, bound);
+      near += score_near(unkey32(k), t, bound);
+    }
+  }
+  sure = __reduce_add_sync(0xffffffffu, sure);
+  near = __reduce_add_sync(0xffffffffu, near);
+  need -= sure;
+  // exact values where there are more near ones than places; a bound of zero
+  // means scores of zero: all tie
+  uint64_t cut64 = 0;
+  int ties = need;
+  const bool rank = near > need && bound > 0.f;
+  if (rank) {
+    double qs[D / 32];
+    exact_query<D>(a, qs, head, n);
+    for (int i = 0; i < places; ++i) {
+      const uint32_t k = key(i);
+      for (uint32_t m = __ballot_sync(0xffffffffu, k != 0 && score_near(unkey32(k), t, bound)); m; m &= m - 1) {
+        const int l = __ffs(m) - 1;
+        const double x = exact_score<D>(a, qs, head, i * 32 + l);
+        if (lane == l) exact[i * 32 + l] = x;       // each lane reads only its own
+      }
+    }
+    auto exact_key = [&](int i) {
+      const uint32_t k = key(i);
+      return k != 0 && score_near(unkey32(k), t, bound) ? key64(exact[i * 32 + lane]) : 0ull;
+    };
+    for (int b = 63; b >= 0; --b) {
+      const uint64_t trial = cut64 | (1ull << b);
       int c = 0;
-#pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        if (i < places) c += key[i] >= trial;
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (c >= need) cut = trial;
-      if (c == need) break;
+      for (int i = 0; i < places; ++i) c += exact_key(i) >= trial;
+      if (__reduce_add_sync(0xffffffffu, c) >= need) cut64 = trial;
     }
-    // the last place's score, and who is near it
-    uint32_t least = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i < places && key[i] >= cut && key[i] != 0) least = min(least, key[i]);
-    low = need > 0 ? __reduce_min_sync(0xffffffffu, least) : 0xFFFFFFFFu;
-    t = unkey32(low);
-    int sure = 0, near = 0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i < places && key[i] != 0) {
-        const float f = unkey32(key[i]);
-        sure += score_above(f, t, bound);
-        near += score_near(f, t, bound);
-      }
-    const int both = __reduce_add_sync(0xffffffffu, sure | (near << 16));
-    sure = both & 0xFFFF;
-    near = both >> 16;
-    border = need > 0 && sure + near > need;
-    if (border) {
-      need -= sure;
-      // near ones get key 1 where they stay, 0 where not; all others are kept or 0
-      double qs[D / 32];
-      if (bound > 0.f) exact_query<D>(a, qs, head, n);
-      if (near <= 32 || !(bound > 0.f)) {
-        // up to 32: lane c holds the c-th one and ranks it against the others.
-        // A bound of zero (query or means of zero): all tie, the first ones stay.
-        double v = 0.0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          if (i >= places) break;
-          const bool is = key[i] != 0 && score_near(unkey32(key[i]), t, bound);
-          uint32_t m = __ballot_sync(0xffffffffu, is);
-          if (!(bound > 0.f)) {
-            if (is) key[i] = at + __popc(m & ((1u << lane) - 1)) < need ? 1u : 0u;
-            at += __popc(m);
-            continue;
-          }
-          if (is) key[i] = 2u + at + __popc(m & ((1u << lane) - 1));    // its holder
-          for (; m; m &= m - 1, ++at) {
-            double x = exact_score<D>(a, qs, head, i * 32 + __ffs(m) - 1);
-            if (x != x) x = -INFINITY;
-            if (lane == at) v = x;
-          }
-        }
-        if (bound > 0.f) {
-          int better = 0;
-          for (int c = 0; c < near; ++c) {
-            const double x = __shfl_sync(0xffffffffu, v, c);
-            better += x > v || (x == v && c < lane);
-          }
-          const uint32_t stay = __ballot_sync(0xffffffffu, lane < near && better < need);
-#pragma unroll
-          for (int i = 0; i < VPL; ++i)
-            if (i < places && key[i] != 0) {
-              if (key[i] - 2u < 32u) key[i] = (stay >> (key[i] - 2u)) & 1u;
-              else if (!score_above(unkey32(key[i]), t, bound)) key[i] = 0;
-            }
-        } else {
-#pragma unroll
-          for (int i = 0; i < VPL; ++i)
-            if (i < places && key[i] > 1u && !score_above(unkey32(key[i]), t, bound)) key[i] = 0;
-        }
-      } else {
-        // many (a flat row): exact values in scratch, each lane its own
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          if (i >= places) break;
-          const bool is = key[i] != 0 && score_near(unkey32(key[i]), t, bound);
-          for (uint32_t m = __ballot_sync(0xffffffffu, is); m; m &= m - 1) {
-            const int l = __ffs(m) - 1;
-            const double x = exact_score<D>(a, qs, head, i * 32 + l);
-            if (lane == l) exact[i * 32 + l] = x;
-          }
-          if (is) key[i] = 1;
-          else if (key[i] != 0 && !score_above(unkey32(key[i]), t, bound)) key[i] = 0;
-        }
-        uint64_t cut64 = 0;
-        for (int b = 63; b >= 0; --b) {
-          const uint64_t trial = cut64 | (1ull << b);
-          int c = 0;
-#pragma unroll
-          for (int i = 0; i < VPL; ++i)
-            if (i < places && key[i] == 1) c += key64(exact[i * 32 + lane]) >= trial;
-          c = __reduce_add_sync(0xffffffffu, c);
-          if (c >= need) cut64 = trial;
-        }
-        int above = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (i < places && key[i] == 1) above += key64(exact[i * 32 + lane]) > cut64;
-        int ties = need - __reduce_add_sync(0xffffffffu, above);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          if (i >= places) break;
-          const uint64_t x = key[i] == 1 ? key64(exact[i * 32 + lane]) : 0ull;
-          const bool tie = key[i] == 1 && x == cut64;
-          const uint32_t m = __ballot_sync(0xffffffffu, tie);
-          if (tie) key[i] = __popc(m & ((1u << lane) - 1)) < ties ? 1u : 0u;
-          else if (key[i] == 1 && x < cut64) key[i] = 0;
-          ties -= min(ties, __popc(m));
-        }
-      }
-    }
+    int better = 0;
+    for (int i = 0; i < places; ++i) better += exact_key(i) > cut64;
+    ties = need - __reduce_add_sync(0xffffffffu, better);
   }
   int at = 0;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    if (i >= places) break;
+  for (int i = 0; i < places; ++i) {
     const int j = i * 32 + lane;
-    const bool keep = (j < r.may && r.forced(j)) || (border ? key[i] != 0 : key[i] >= low);
+    const uint32_t k = key(i);
+    const float f = unkey32(k);
+    bool keep = j < r.may && r.forced(j), tie = false;
+    if (k != 0 && a.topk > r.num_forced()) {
+      keep = score_above(f, t, bound);
+      if (!keep && score_near(f, t, bound)) {
+        const uint64_t x = rank ? key64(exact[j]) : 0ull;
+        keep = rank && x > cut64;
+        tie = !rank || x == cut64;
+      }
+    }
+    const uint32_t tied = __ballot_sync(0xffffffffu, tie);
+    if (tie) keep = __popc(tied & ((1u << lane) - 1)) < ties;
+    ties -= min(ties, __popc(tied));
     const uint32_t m = __ballot_sync(0xffffffffu, keep);
     if (keep) out[at + __popc(m & ((1u << lane) - 1))] = j;
     at += __popc(m);
@@ -319,8 +423,10 @@ __device__ void select_row(const SelectArgs &a, const float *s, double *exact, f
 // are at most 2^-16 of a product, the roundings of the fp32 sums (24 matrix
 // steps) less than 2^-17, so the error is below 2^-14 |q| |mean| (norms of the
 // head-wise absolute sum and of the block's mean).  The queries' parts stay in
-// registers, the means' stream through two buffers; the scores go to the CTA's
-// own scratch rows (read back from L2) and a warp per row picks.
+// registers, the means' stream through two buffers, and the scores go to
+// scratch rows.  A second kernel with a warp per row picks; it needs few
+// registers, so four times as many warps hide its latencies.  Both run over
+// parts of the queries whose scores stay in L2.
 constexpr int kSelTile = 64, kSelThreads = 128;
 constexpr float kSelSplitError = 1.f / 16384.f;
 
@@ -375,23 +481,34 @@ __global__ void __launch_bounds__(256) block_select_split_kernel(const SelectArg
   if (threadIdx.x == 0) a.tile_norm[blockIdx.x] = __uint_as_float(mn);
 }
 
-template <int D, int VPL>
-__global__ void __launch_bounds__(kSelThreads, VPL <= 32 ? 3 : 2) block_select_kernel(const SelectArgs a) {
+// An item is a tile of 64 queries of a key head; the last ones come first (long
+// causal rows).
+struct SelectItem {
+  int head, n0, len;
+};
+__device__ __forceinline__ SelectItem select_item(const SelectArgs &a, int item) {
+  const int qtiles = (a.Nq + kSelTile - 1) / kSelTile;
+  SelectItem x;
+  x.head = item % a.BHk;
+  x.n0 = (qtiles - 1 - item / a.BHk) * kSelTile;
+  x.len = seq_len(a.kv_len, x.head / a.heads_per_seq, a.Nk);
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kSelThreads, 3) block_select_score_kernel(const SelectArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float qn[kSelTile];       // |q| of every row
   constexpr int TILE = kSelTile * D * 2, COLS = D / 8;
   const uint32_t base = smem_u32(smem);
   const int warp = warp_id();
-  const int qtiles = (a.Nq + kSelTile - 1) / kSelTile, tiles = (a.nblk + kSelTile - 1) / kSelTile;
-  const int64_t items = static_cast<int64_t>(qtiles) * a.BHk;
-  float *scores = a.scores + static_cast<int64_t>(blockIdx.x) * kSelTile * a.nblk;
-  double *exact = a.exact + (static_cast<int64_t>(blockIdx.x) * (kSelThreads / 32) + warp) * a.nblk;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-    const int head = static_cast<int>(item % a.BHk);
-    const int n0 = (qtiles - 1 - static_cast<int>(item / a.BHk)) * kSelTile;    // long causal rows first
-    const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
-    const int last = min(n0 + kSelTile, a.Nq) - 1;
-    const int most = select_range(a, len, last).may;
+  const int tiles = (a.nblk + kSelTile - 1) / kSelTile;
+  const int wide = tiles * kSelTile;   // a scratch row
+  float *scores = a.scores + static_cast<int64_t>(blockIdx.x) * kSelTile * wide;
+  const SelectItem item = select_item(a, a.item0 + blockIdx.x);
+  const int head = item.head, n0 = item.n0, len = item.len;
+  {
+    const int most = select_range(a, len, min(n0 + kSelTile, a.Nq) - 1).may;
     const __nv_bfloat16 *hi = a.mean_hi + static_cast<int64_t>(head) * tiles * kSelTile * D;
     const __nv_bfloat16 *lo = a.mean_lo + static_cast<int64_t>(head) * tiles * kSelTile * D;
     auto fetch = [&](int t) {          // tile t of the means' parts
@@ -417,14 +534,22 @@ __global__ void __launch_bounds__(kSelThreads, VPL <= 32 ? 3 : 2) block_select_k
         float w[8], z[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = 0.f;
-        for (int g = 0; g < a.G; ++g) {
-          unpack8(__ldg(reinterpret_cast<const uint4 *>(
-                      a.q + ((static_cast<int64_t>(head) * a.G + g) * a.Nq + n0 + r) * D + 8 * c)),
-                  w);
+        const __nv_bfloat16 *src = a.q + (static_cast<int64_t>(head) * a.G * a.Nq + n0 + r) * D + 8 * c;
+        for (int g0 = 0; g0 < a.G; g0 += 8) {       // 8 loads in flight
+          uint4 x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            f[e] += w[e];
-            z[e] += fabsf(w[e]);
+          for (int g = 0; g < 8; ++g)
+            x[g] = g0 + g < a.G ? __ldg(reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(g0 + g) * a.Nq * D))
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            if (g0 + g >= a.G) break;
+            unpack8(x[g], w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              f[e] += w[e];
+              z[e] += fabsf(w[e]);
+            }
           }
         }
 #pragma unroll
@@ -462,39 +587,53 @@ __global__ void __launch_bounds__(kSelThreads, VPL <= 32 ? 3 : 2) block_select_k
         for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
+        // eight independent sums between two steps of one
+        uint32_t bh[4][4], bl[4][4];
 #pragma unroll
-        for (int t = 0; t < 8; t += 2) {
-          uint32_t bh[4], bl[4];
-          ldsm_x4(ldsm_b<D>(m_hi, 8 * t, ks), bh);
-          ldsm_x4(ldsm_b<D>(m_lo, 8 * t, ks), bl);
-          mma_bf16(acc[t], al[ks], bh[0], bh[1]);
-          mma_bf16(acc[t + 1], al[ks], bh[2], bh[3]);
-          mma_bf16(acc[t], ah[ks], bl[0], bl[1]);
-          mma_bf16(acc[t + 1], ah[ks], bl[2], bl[3]);
-          mma_bf16(acc[t], ah[ks], bh[0], bh[1]);
-          mma_bf16(acc[t + 1], ah[ks], bh[2], bh[3]);
+        for (int t = 0; t < 4; ++t) {
+          ldsm_x4(ldsm_b<D>(m_hi, 16 * t, ks), bh[t]);
+          ldsm_x4(ldsm_b<D>(m_lo, 16 * t, ks), bl[t]);
         }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mma_bf16(acc[t], al[ks], bh[t / 2][2 * (t & 1)], bh[t / 2][2 * (t & 1) + 1]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mma_bf16(acc[t], ah[ks], bl[t / 2][2 * (t & 1)], bl[t / 2][2 * (t & 1) + 1]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) mma_bf16(acc[t], ah[ks], bh[t / 2][2 * (t & 1)], bh[t / 2][2 * (t & 1) + 1]);
       }
-      const int r0 = 16 * warp + frag_row();
+      float *row = scores + static_cast<int64_t>(16 * warp + frag_row()) * wide + j0 + frag_col();
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = r0 + (e >> 1) * 8, j = j0 + 8 * t + frag_col() + (e & 1);
-          if (j < most) scores[static_cast<int64_t>(r) * a.nblk + j] = acc[t][e];
-        }
+      for (int t = 0; t < 8; ++t) {
+        *reinterpret_cast<float2 *>(row + 8 * t) = make_float2(acc[t][0], acc[t][1]);
+        *reinterpret_cast<float2 *>(row + 8 * wide + 8 * t) = make_float2(acc[t][2], acc[t][3]);
+      }
       __syncthreads();
     }
-    // a warp reads only the rows that it wrote
-    norm = sqrtf(norm);
-    for (int r = 16 * warp; r < 16 * warp + 16 && n0 + r < a.Nq; ++r) {
-      float bound = kSelSplitError * qn[r] * norm;
-      if (!(bound <= 3.4e38f)) bound = INFINITY;
-      select_row<D, VPL>(a, scores + static_cast<int64_t>(r) * a.nblk, exact, bound, head, n0 + r,
-                         select_range(a, len, n0 + r));
-      __syncwarp();
+    if (threadIdx.x < kSelTile) {
+      const float bound = kSelSplitError * qn[threadIdx.x] * sqrtf(norm);
+      a.bounds[blockIdx.x * kSelTile + threadIdx.x] = bound <= 3.4e38f ? bound : INFINITY;
     }
-    __syncthreads();
+  }
+}
+
+// Picks: a warp per row, `gridDim.x` CTAs in turn over the part's rows.
+template <int D, int VPL>
+__global__ void __launch_bounds__(kSelThreads, VPL <= 16 ? 6 : VPL <= 32 ? 5 : 3) block_select_pick_kernel(const SelectArgs a) {
+  constexpr int WARPS = kSelThreads / 32;
+  __shared__ int near[WARPS][32];
+  const int wide = (a.nblk + kSelTile - 1) / kSelTile * kSelTile, warp = warp_id();
+  double *exact = a.exact + (static_cast<int64_t>(blockIdx.x) * WARPS + warp) * a.nblk;
+  const int rows = a.items * kSelTile;
+  for (int row = blockIdx.x * WARPS + warp; row < rows; row += gridDim.x * WARPS) {
+    const SelectItem item = select_item(a, a.item0 + row / kSelTile);
+    const int n = item.n0 + row % kSelTile;
+    if (n >= a.Nq) continue;
+    const SelectRange range = select_range(a, item.len, n);
+    const float *s = a.scores + static_cast<int64_t>(row) * wide;
+    const float bound = a.bounds[row];
+    if (!select_row<D, VPL>(a, s, near[warp], bound, item.head, n, range))
+      select_row_any<D>(a, s, exact, bound, item.head, n, range);
+    __syncwarp();
   }
 }
 

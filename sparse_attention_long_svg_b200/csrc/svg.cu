@@ -989,18 +989,32 @@ svg_status block_shapes(int BHq, int BHk, int B, int Nq, int Nk, int D, int bloc
 // block_select: few queries take the kernel with one CTA per query (it reads a
 // head's means once per query), more the one with 64 queries per CTA.
 bool select_few(int Nq) { return Nq <= 4; }
-int select_ctas(int BHk, int Nq) {
-  const int64_t items = static_cast<int64_t>(BHk) * ((Nq + kSelTile - 1) / kSelTile);
-  const int64_t most = 3ll * num_sms();
-  return static_cast<int>(items < most ? items : most);
+int64_t select_items(int BHk, int Nq) { return static_cast<int64_t>(BHk) * ((Nq + kSelTile - 1) / kSelTile); }
+// Items of a part: a multiple of what runs at a time (3 per SM) whose scores take
+// at most 64 MiB, half of L2.
+constexpr int64_t kSelPartBytes = 64ll << 20;
+int64_t select_part(int BHk, int Nq, int nblk) {
+  const int64_t row = (nblk + kSelTile - 1) / kSelTile * kSelTile * sizeof(float);
+  const int64_t wave = 3ll * num_sms();
+  int64_t part = kSelPartBytes / (row * kSelTile) / wave * wave;
+  if (part < wave) part = wave;
+  const int64_t items = select_items(BHk, Nq);
+  return part < items ? part : items;
+}
+int select_pick_ctas(int64_t part) {
+  const int64_t most = 16ll * num_sms(), rows = part * kSelTile * 32 / kSelThreads;
+  return static_cast<int>(rows < most ? rows : most);
 }
 
 SelectArgs carve_select(void *ws, int BHk, int Nq, int nblk, int D, size_t *bytes) {
   Carve c{static_cast<uint8_t *>(ws)};
   SelectArgs a{};
-  const size_t tiles = (nblk + kSelTile - 1) / kSelTile, ctas = select_ctas(BHk, Nq);
-  a.exact = c.take<double>(ctas * (kSelThreads / 32) * nblk);
-  a.scores = c.take<float>(ctas * kSelTile * nblk);
+  const size_t tiles = (nblk + kSelTile - 1) / kSelTile;
+  const size_t part = select_part(BHk, Nq, nblk);
+  a.items = static_cast<int>(part);
+  a.exact = c.take<double>(static_cast<size_t>(select_pick_ctas(part)) * (kSelThreads / 32) * nblk);
+  a.scores = c.take<float>(part * kSelTile * tiles * kSelTile);
+  a.bounds = c.take<float>(part * kSelTile);
   a.mean_hi = c.take<__nv_bfloat16>(BHk * tiles * kSelTile * D);
   a.mean_lo = c.take<__nv_bfloat16>(BHk * tiles * kSelTile * D);
   a.tile_norm = c.take<float>(BHk * tiles);
@@ -1157,25 +1171,31 @@ svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, 
     return D == 128 ? one(block_select_decode_kernel<128>) : one(block_select_decode_kernel<64>);
   }
   const int tiles = (nblk + kSelTile - 1) / kSelTile;
-  auto many = [&](auto split, auto kernel, size_t smem) {
-    if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
+  auto many = [&](auto split, auto score, size_t smem, auto pick) {
+    if (!set_smem(score, smem)) return SVG_ERR_CUDA;
     split<<<BHk * tiles, 256, 0, s>>>(a, tiles);
-    kernel<<<select_ctas(BHk, Nq), kSelThreads, smem, s>>>(a);
+    const int items = static_cast<int>(select_items(BHk, Nq)), part = a.items;
+    for (a.item0 = 0; a.item0 < items; a.item0 += part) {
+      a.items = items - a.item0 < part ? items - a.item0 : part;
+      score<<<a.items, kSelThreads, smem, s>>>(a);
+      pick<<<select_pick_ctas(part), kSelThreads, 0, s>>>(a);
+    }
     return launch_status("block_select_kernel");
   };
   // places of a lane: a row's keys stay in registers
-  if (D == 128) {
-    auto split = block_select_split_kernel<128>;
-    if (nblk <= 128) return many(split, block_select_kernel<128, 4>, select_smem<128>());
-    if (nblk <= 512) return many(split, block_select_kernel<128, 16>, select_smem<128>());
-    if (nblk <= 1024) return many(split, block_select_kernel<128, 32>, select_smem<128>());
-    return many(split, block_select_kernel<128, 128>, select_smem<128>());
-  }
-  auto split = block_select_split_kernel<64>;
-  if (nblk <= 128) return many(split, block_select_kernel<64, 4>, select_smem<64>());
-  if (nblk <= 512) return many(split, block_select_kernel<64, 16>, select_smem<64>());
-  if (nblk <= 1024) return many(split, block_select_kernel<64, 32>, select_smem<64>());
-  return many(split, block_select_kernel<64, 128>, select_smem<64>());
+  auto by_places = [&](auto split, auto score, size_t smem, auto p4, auto p16, auto p32, auto p128) {
+    if (nblk <= 128) return many(split, score, smem, p4);
+    if (nblk <= 512) return many(split, score, smem, p16);
+    if (nblk <= 1024) return many(split, score, smem, p32);
+    return many(split, score, smem, p128);
+  };
+  if (D == 128)
+    return by_places(block_select_split_kernel<128>, block_select_score_kernel<128>, select_smem<128>(),
+                     block_select_pick_kernel<128, 4>, block_select_pick_kernel<128, 16>,
+                     block_select_pick_kernel<128, 32>, block_select_pick_kernel<128, 128>);
+  return by_places(block_select_split_kernel<64>, block_select_score_kernel<64>, select_smem<64>(),
+                   block_select_pick_kernel<64, 4>, block_select_pick_kernel<64, 16>, block_select_pick_kernel<64, 32>,
+                   block_select_pick_kernel<64, 128>);
 }
 
 size_t svg_block_attn_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block) {
