@@ -94,16 +94,23 @@ __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int
   return *count;
 }
 
-// Rows [key0, key0 + 64) of a [Nk, D] matrix to a shared tile by `threads`
+// Rows [key0, key0 + 64) of a [Nk, D] matrix to a shared tile by THREADS
 // threads; rows from `len` on become zeros.
-template <int D>
-__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *src, int key0, int len, int tid,
-                                          int threads) {
-  constexpr int COLS = D / 8;
-  for (int i = tid; i < kBaTile * COLS; i += threads) {
-    const int r = i / COLS, c = i % COLS;
-    const bool in = key0 + r < len;
-    cp_async16(dst + tile_at<D>(r, c), src + (in ? static_cast<int64_t>(key0 + r) * D + 8 * c : 0), in ? 16u : 0u);
+template <int D, int THREADS>
+__device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *src, int key0, int len, int tid) {
+  constexpr int COLS = D / 8, STEP = THREADS / COLS;       // STEP rows at a time
+  static_assert(STEP % 2 == 0 && kBaTile % STEP == 0, "");
+  const int r0 = tid / COLS, c = tid % COLS;
+  const __nv_bfloat16 *from = src + static_cast<int64_t>(key0 + r0) * D + 8 * c;
+  if (key0 + kBaTile <= len) {
+#pragma unroll
+    for (int r = 0; r < kBaTile; r += STEP) cp_async16(dst + tile_at<D>(r0 + r, c), from + r * D, 16);
+  } else {
+#pragma unroll
+    for (int r = 0; r < kBaTile; r += STEP) {
+      const bool in = key0 + r0 + r < len;
+      cp_async16(dst + tile_at<D>(r0 + r, c), in ? from + r * D : src, in ? 16u : 0u);
+    }
   }
 }
 
@@ -151,8 +158,8 @@ __host__ __device__ inline size_t block_attn_smem(int tiles, int tokens, int nbl
 // take every fourth tile, each through its own buffer; the CTA joins them.
 // gridDim.y splits the union's tiles; a second kernel joins the splits.
 template <int D, bool FEW>
-__global__ void __launch_bounds__(kBaThreads) block_attn_kernel(const BlockAttnArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
+__global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(const BlockAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int TILE = kBaTile * D * 2, NT = D / 8;
   constexpr int TILES = FEW ? 8 : 4;
   const int per = 16 / a.G;                       // tokens of a warp
@@ -188,16 +195,19 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_kernel(const BlockAttnA
 
   const uint32_t base = smem_u32(smem);
   const int first = FEW ? u0 + warp : u0, step = FEW ? 4 : 1;
-  const int tid = FEW ? static_cast<int>(lane_id()) : static_cast<int>(threadIdx.x);
-  const int nthr = FEW ? 32 : kBaThreads;
   auto buffer = [&](int i) { return base + static_cast<uint32_t>(FEW ? warp : (i & 1)) * 2 * TILE; };
   auto key_of = [&](int u) { return static_cast<int>(list[u / sub]) * a.block + (u % sub) * kBaTile; };
   auto fetch = [&](int i) {
     const int u = first + i * step;
     if (u < u1) {
       const int key0 = key_of(u);
-      load_tile<D>(buffer(i), kh, key0, len, tid, nthr);
-      load_tile<D>(buffer(i) + TILE, vh, key0, len, tid, nthr);
+      if (FEW) {
+        load_tile<D, 32>(buffer(i), kh, key0, len, lane_id());
+        load_tile<D, 32>(buffer(i) + TILE, vh, key0, len, lane_id());
+      } else {
+        load_tile<D, kBaThreads>(buffer(i), kh, key0, len, threadIdx.x);
+        load_tile<D, kBaThreads>(buffer(i) + TILE, vh, key0, len, threadIdx.x);
+      }
     }
     cp_async_commit();
   };
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_kernel(const BlockAttnA
     const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
     const bool on1 = x1.row >= 0 && ((bits[x1.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x1.seen;
     if (__any_sync(0xffffffffu, on0 || on1)) {
-      const uint32_t kt = buffer(i), vt = kt + TILE;
+      const uint32_t kt = lane_b<D>(buffer(i)), vt = lane_a<D>(buffer(i) + TILE);
       float s[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -227,60 +237,87 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_kernel(const BlockAttnA
 #pragma unroll
         for (int t = 0; t < 8; t += 2) {
           uint32_t b[4];
-          ldsm_x4(ldsm_b<D>(kt, 8 * t, ks), b);
+          ldsm_x4(piece<D>(kt, 8 * t, ks), b);
           mma_bf16(s[t], qf[ks], b[0], b[1]);
           mma_bf16(s[t + 1], qf[ks], b[2], b[3]);
         }
       const int end0 = on0 ? x0.seen - key0 : 0, end1 = on1 ? x1.seen - key0 : 0;
+      if (!__all_sync(0xffffffffu, end0 >= kBaTile && end1 >= kBaTile)) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const int c = 8 * t + frag_col();
+          s[t][0] = c < end0 ? s[t][0] : -INFINITY;
+          s[t][1] = c + 1 < end0 ? s[t][1] : -INFINITY;
+          s[t][2] = c < end1 ? s[t][2] : -INFINITY;
+          s[t][3] = c + 1 < end1 ? s[t][3] : -INFINITY;
+        }
+      }
       float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const int c = 8 * t + frag_col();
-        s[t][0] = c < end0 ? s[t][0] * a.scale_log2 : -INFINITY;
-        s[t][1] = c + 1 < end0 ? s[t][1] * a.scale_log2 : -INFINITY;
-        s[t][2] = c < end1 ? s[t][2] * a.scale_log2 : -INFINITY;
-        s[t][3] = c + 1 < end1 ? s[t][3] * a.scale_log2 : -INFINITY;
         t0 = fmaxf(t0, fmaxf(s[t][0], s[t][1]));
         t1 = fmaxf(t1, fmaxf(s[t][2], s[t][3]));
       }
-      const float n0m = fmaxf(m0, quad_max(t0)), n1m = fmaxf(m1, quad_max(t1));
+      const float n0m = fmaxf(m0, quad_max(t0) * a.scale_log2), n1m = fmaxf(m1, quad_max(t1) * a.scale_log2);
       const float b0 = n0m == -INFINITY ? 0.f : n0m, b1 = n1m == -INFINITY ? 0.f : n1m;
-      const float f0 = on0 ? ex2_approx(m0 - b0) : 1.f, f1 = on1 ? ex2_approx(m1 - b1) : 1.f;
-      m0 = n0m;
-      m1 = n1m;
-      l0 *= f0;
-      l1 *= f1;
+      if (__any_sync(0xffffffffu, n0m != m0 || n1m != m1)) {      // a new maximum: rescale
+        const float f0 = n0m != m0 ? ex2_approx(m0 - b0) : 1.f, f1 = n1m != m1 ? ex2_approx(m1 - b1) : 1.f;
+        m0 = n0m;
+        m1 = n1m;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          acc[t][0] *= f0;
+          acc[t][1] *= f0;
+          acc[t][2] *= f1;
+          acc[t][3] *= f1;
+        }
+      }
       uint32_t p[4][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const float p0 = ex2_approx(s[t][0] - b0), p1 = ex2_approx(s[t][1] - b0);
-        const float p2 = ex2_approx(s[t][2] - b1), p3 = ex2_approx(s[t][3] - b1);
+        const float p0 = ex2_approx(fmaf(s[t][0], a.scale_log2, -b0)), p1 = ex2_approx(fmaf(s[t][1], a.scale_log2, -b0));
+        const float p2 = ex2_approx(fmaf(s[t][2], a.scale_log2, -b1)), p3 = ex2_approx(fmaf(s[t][3], a.scale_log2, -b1));
         l0 += p0 + p1;
         l1 += p2 + p3;
         // P as bf16 for the matrix product: 2^-8 relative to each weight; the sum keeps fp32
         p[t / 2][(t & 1) * 2] = pack_bf16(p0, p1);
         p[t / 2][(t & 1) * 2 + 1] = pack_bf16(p2, p3);
       }
+      if (__all_sync(0xffffffffu, on0 && on1)) {
 #pragma unroll
-      for (int t = 0; t < NT; t += 2) {
-        float c0[4] = {acc[t][0] * f0, acc[t][1] * f0, acc[t][2] * f1, acc[t][3] * f1};
-        float c1[4] = {acc[t + 1][0] * f0, acc[t + 1][1] * f0, acc[t + 1][2] * f1, acc[t + 1][3] * f1};
+        for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          uint32_t b[4];
-          ldsm_x4_trans(ldsm_a<D>(vt, 16 * ks, t / 2), b);
-          mma_bf16(c0, p[ks], b[0], b[1]);
-          mma_bf16(c1, p[ks], b[2], b[3]);
-        }
+          for (int t = 0; t < NT; t += 2) {
+            uint32_t b[4];
+            ldsm_x4_trans(piece<D>(vt, 16 * ks, t / 2), b);
+            mma_bf16(acc[t], p[ks], b[0], b[1]);
+            mma_bf16(acc[t + 1], p[ks], b[2], b[3]);
+          }
+      } else {
         // a row that does not list this block keeps its accumulator, whatever V holds
-        acc[t][0] = on0 ? c0[0] : acc[t][0];
-        acc[t][1] = on0 ? c0[1] : acc[t][1];
-        acc[t][2] = on1 ? c0[2] : acc[t][2];
-        acc[t][3] = on1 ? c0[3] : acc[t][3];
-        acc[t + 1][0] = on0 ? c1[0] : acc[t + 1][0];
-        acc[t + 1][1] = on0 ? c1[1] : acc[t + 1][1];
-        acc[t + 1][2] = on1 ? c1[2] : acc[t + 1][2];
-        acc[t + 1][3] = on1 ? c1[3] : acc[t + 1][3];
+#pragma unroll
+        for (int t = 0; t < NT; t += 4) {
+          float c[4][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[j][e] = acc[t + j][e];
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              uint32_t b[4];
+              ldsm_x4_trans(piece<D>(vt, 16 * ks, (t + j) / 2), b);
+              mma_bf16(c[j], p[ks], b[0], b[1]);
+              mma_bf16(c[j + 1], p[ks], b[2], b[3]);
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t + j][e] = (e < 2 ? on0 : on1) ? c[j][e] : acc[t + j][e];
+        }
       }
     }
     if (FEW) {
@@ -412,7 +449,7 @@ __global__ void __launch_bounds__(128) block_attn_join_kernel(const BlockAttnArg
 // products per tile, 32 keys at a time to stay in registers.
 template <int D>
 __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAttnArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int TILE = kBaTile * D * 2, NT = D / 8;
   const int per = 16 / a.G, tokens = 4 * per;
   const int ntiles = (a.Nq + tokens - 1) / tokens;
@@ -463,8 +500,8 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
   auto fetch = [&](int u) {
     if (u < total) {
       const uint32_t buf = base + static_cast<uint32_t>(u & 1) * 2 * TILE;
-      load_tile<D>(buf, kh, key_of(u), len, threadIdx.x, kBaThreads);
-      load_tile<D>(buf + TILE, vh, key_of(u), len, threadIdx.x, kBaThreads);
+      load_tile<D, kBaThreads>(buf, kh, key_of(u), len, threadIdx.x);
+      load_tile<D, kBaThreads>(buf + TILE, vh, key_of(u), len, threadIdx.x);
     }
     cp_async_commit();
   };
@@ -477,7 +514,8 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
     const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
     const bool on1 = x1.row >= 0 && ((bits[x1.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x1.seen;
     if (__any_sync(0xffffffffu, on0 || on1)) {
-      const uint32_t kt = base + static_cast<uint32_t>(u & 1) * 2 * TILE, vt = kt + TILE;
+      const uint32_t tile = base + static_cast<uint32_t>(u & 1) * 2 * TILE;
+      const uint32_t kt = lane_b<D>(tile), vt = kt + TILE, kx = lane_a<D>(tile);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float s[4][4], dp[4][4];
@@ -490,10 +528,10 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
 #pragma unroll
           for (int t = 0; t < 4; t += 2) {
             uint32_t b[4];
-            ldsm_x4(ldsm_b<D>(kt, 32 * h + 8 * t, ks), b);
+            ldsm_x4(piece<D>(kt, 32 * h + 8 * t, ks), b);
             mma_bf16(s[t], qf[ks], b[0], b[1]);
             mma_bf16(s[t + 1], qf[ks], b[2], b[3]);
-            ldsm_x4(ldsm_b<D>(vt, 32 * h + 8 * t, ks), b);
+            ldsm_x4(piece<D>(vt, 32 * h + 8 * t, ks), b);
             mma_bf16(dp[t], df[ks], b[0], b[1]);
             mma_bf16(dp[t + 1], df[ks], b[2], b[3]);
           }
@@ -513,22 +551,25 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
           ds[t / 2][(t & 1) * 2 + 1] = pack_bf16(g[2], g[3]);
         }
 #pragma unroll
-        for (int t = 0; t < NT; t += 2) {
-          float c0[4] = {acc[t][0], acc[t][1], acc[t][2], acc[t][3]};
-          float c1[4] = {acc[t + 1][0], acc[t + 1][1], acc[t + 1][2], acc[t + 1][3]};
+        for (int t = 0; t < NT; t += 4) {
+          float c[4][4];
 #pragma unroll
-          for (int ks = 0; ks < 2; ++ks) {
-            uint32_t b[4];
-            ldsm_x4_trans(ldsm_a<D>(kt, 32 * h + 16 * ks, t / 2), b);
-            mma_bf16(c0, ds[ks], b[0], b[1]);
-            mma_bf16(c1, ds[ks], b[2], b[3]);
-          }
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool on = e < 2 ? on0 : on1;
-            acc[t][e] = on ? c0[e] : acc[t][e];
-            acc[t + 1][e] = on ? c1[e] : acc[t + 1][e];
-          }
+            for (int e = 0; e < 4; ++e) c[j][e] = acc[t + j][e];
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              uint32_t b[4];
+              ldsm_x4_trans(piece<D>(kx, 32 * h + 16 * ks, (t + j) / 2), b);
+              mma_bf16(c[j], ds[ks], b[0], b[1]);
+              mma_bf16(c[j + 1], ds[ks], b[2], b[3]);
+            }
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t + j][e] = (e < 2 ? on0 : on1) ? c[j][e] : acc[t + j][e];
         }
       }
     }
@@ -621,7 +662,7 @@ __host__ __device__ inline size_t block_attn_dkv_smem(int item_tokens) {
 
 template <int D>
 __global__ void __launch_bounds__(kBaThreads) block_attn_dkv_kernel(const BlockAttnArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int TILE = kBaRows * D * 2, NT = D / 8, COLS = D / 8;
   const int sub = a.block / kBaTile;
   const int tiles = a.BHk * a.nblk * sub;
@@ -639,8 +680,8 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dkv_kernel(const BlockA
   float *row_lse = reinterpret_cast<float *>(smem + 4 * TILE);      // [2][64]
   float *row_delta = row_lse + 2 * kBaRows;
   int *row_seen = reinterpret_cast<int *>(row_delta + 2 * kBaRows);
-  int *toks = row_seen + 2 * kBaRows;
-  __shared__ int warp_sum[4];
+  int *warp_sum = row_seen + 2 * kBaRows;      // [4]
+  int *toks = warp_sum + 4;
 
   // this item's queries: places [skip, skip + item_tokens) of the block's bit set
   const int skip = (item - first) * a.item_tokens;
@@ -718,7 +759,8 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dkv_kernel(const BlockA
     fetch(r0 + kBaRows, st ^ 1);
     cp_async_wait<1>();
     __syncthreads();
-    const uint32_t qt = base + static_cast<uint32_t>(st) * 2 * TILE, dt = qt + TILE;
+    const uint32_t tile = base + static_cast<uint32_t>(st) * 2 * TILE;
+    const uint32_t qb = lane_b<D>(tile), qa = lane_a<D>(tile);      // dO's tile lies behind Q's
 #pragma unroll 1
     for (int rs = 0; rs < kBaRows; rs += 16) {
       if (r0 + rs >= rows) break;
@@ -730,10 +772,10 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dkv_kernel(const BlockA
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         uint32_t b[4];
-        ldsm_x4(ldsm_b<D>(qt, rs, ks), b);
+        ldsm_x4(piece<D>(qb, rs, ks), b);
         mma_bf16(s[0], kf[ks], b[0], b[1]);
         mma_bf16(s[1], kf[ks], b[2], b[3]);
-        ldsm_x4(ldsm_b<D>(dt, rs, ks), b);
+        ldsm_x4(piece<D>(qb + TILE, rs, ks), b);
         mma_bf16(dp[0], vf[ks], b[0], b[1]);
         mma_bf16(dp[1], vf[ks], b[2], b[3]);
       }
@@ -756,10 +798,10 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dkv_kernel(const BlockA
 #pragma unroll
       for (int t = 0; t < NT; t += 2) {
         uint32_t b[4];
-        ldsm_x4_trans(ldsm_a<D>(dt, rs, t / 2), b);
+        ldsm_x4_trans(piece<D>(qa + TILE, rs, t / 2), b);
         mma_bf16(dv[t], pf, b[0], b[1]);
         mma_bf16(dv[t + 1], pf, b[2], b[3]);
-        ldsm_x4_trans(ldsm_a<D>(qt, rs, t / 2), b);
+        ldsm_x4_trans(piece<D>(qa, rs, t / 2), b);
         mma_bf16(dk[t], gf, b[0], b[1]);
         mma_bf16(dk[t + 1], gf, b[2], b[3]);
       }

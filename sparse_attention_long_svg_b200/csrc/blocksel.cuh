@@ -432,7 +432,7 @@ constexpr float kSelSplitError = 1.f / 16384.f;
 
 template <int D>
 constexpr int select_smem() {
-  return 4 * kSelTile * D * 2;
+  return 4 * kSelTile * D * 2 + kSelTile * 4;
 }
 
 __device__ __forceinline__ void split8(const float (&f)[8], uint4 &hi, uint4 &lo) {
@@ -497,9 +497,9 @@ __device__ __forceinline__ SelectItem select_item(const SelectArgs &a, int item)
 
 template <int D>
 __global__ void __launch_bounds__(kSelThreads, 3) block_select_score_kernel(const SelectArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float qn[kSelTile];       // |q| of every row
+  extern __shared__ __align__(1024) uint8_t smem[];
   constexpr int TILE = kSelTile * D * 2, COLS = D / 8;
+  float *qn = reinterpret_cast<float *>(smem + 4 * TILE);      // |q| of every row
   const uint32_t base = smem_u32(smem);
   const int warp = warp_id();
   const int tiles = (a.nblk + kSelTile - 1) / kSelTile;
@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) block_select_score_kernel(cons
     uint32_t ah[D / 16][4], al[D / 16][4];
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      ldsm_x4(ldsm_a<D>(base + 2 * TILE, 16 * warp, ks), ah[ks]);
-      ldsm_x4(ldsm_a<D>(base + 3 * TILE, 16 * warp, ks), al[ks]);
+      ldsm_x4(piece<D>(lane_a<D>(base + 2 * TILE), 16 * warp, ks), ah[ks]);
+      ldsm_x4(piece<D>(lane_a<D>(base + 3 * TILE), 16 * warp, ks), al[ks]);
     }
     __syncthreads();
     float norm = 0.f;
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) block_select_score_kernel(cons
       fetch(tile + 1);
       cp_async_wait<1>();
       __syncthreads();
-      const uint32_t m_hi = base + static_cast<uint32_t>(tile & 1) * 2 * TILE, m_lo = m_hi + TILE;
+      const uint32_t m_hi = lane_b<D>(base + static_cast<uint32_t>(tile & 1) * 2 * TILE), m_lo = m_hi + TILE;
       float acc[8][4];
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -591,8 +591,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) block_select_score_kernel(cons
         uint32_t bh[4][4], bl[4][4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          ldsm_x4(ldsm_b<D>(m_hi, 16 * t, ks), bh[t]);
-          ldsm_x4(ldsm_b<D>(m_lo, 16 * t, ks), bl[t]);
+          ldsm_x4(piece<D>(m_hi, 16 * t, ks), bh[t]);
+          ldsm_x4(piece<D>(m_lo, 16 * t, ks), bl[t]);
         }
 #pragma unroll
         for (int t = 0; t < 8; ++t) mma_bf16(acc[t], al[ks], bh[t / 2][2 * (t & 1)], bh[t / 2][2 * (t & 1) + 1]);

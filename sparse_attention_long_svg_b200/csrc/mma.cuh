@@ -53,23 +53,33 @@ __device__ __forceinline__ uint32_t tile_at(int r, int ch) {
   return static_cast<uint32_t>(r * (D * 2) + ((ch ^ (r & 7)) << 4));
 }
 
-// Address this lane gives to an ldmatrix.x4 of the 16 x 16 piece at row r0,
-// channel 16 * ks: matrices (rows 0-7, ch 0-7), (rows 8-15, ch 0-7),
-// (rows 0-7, ch 8-15), (rows 8-15, ch 8-15) = the four registers of an A
-// operand; with .trans the two B operands of 16 rows x (2 x 8) channels.
+// This lane's address for an ldmatrix.x4 of a 16 x 16 piece of a tile (at its
+// row 0, channel 0): matrices (rows 0-7, ch 0-7), (rows 8-15, ch 0-7), (rows 0-7,
+// ch 8-15), (rows 8-15, ch 8-15) = the four registers of an A operand; with
+// .trans the two B operands of 16 rows x (2 x 8) channels.
 template <int D>
-__device__ __forceinline__ uint32_t ldsm_a(uint32_t tile, int r0, int ks) {
+__device__ __forceinline__ uint32_t lane_a(uint32_t tile) {
   const int l = lane_id();
-  return tile + tile_at<D>(r0 + (l & 15), 2 * ks + (l >> 4));
+  return tile + tile_at<D>(l & 15, l >> 4);
 }
 
-// The same piece with the middle matrices exchanged: without .trans registers
-// 0, 1 are the B operand of rows 0-7 and 2, 3 that of rows 8-15 (contraction
-// over the 16 channels).
+// The same with the middle matrices exchanged: without .trans registers 0, 1
+// are the B operand of rows 0-7 and 2, 3 that of rows 8-15 (contraction over
+// the 16 channels).
 template <int D>
-__device__ __forceinline__ uint32_t ldsm_b(uint32_t tile, int r0, int ks) {
+__device__ __forceinline__ uint32_t lane_b(uint32_t tile) {
   const int l = lane_id();
-  return tile + tile_at<D>(r0 + (l & 7) + ((l >> 4) << 3), 2 * ks + ((l >> 3) & 1));
+  return tile + tile_at<D>((l & 7) + ((l >> 4) << 3), (l >> 3) & 1);
+}
+
+// From such an address to the piece at row r0 (a multiple of 8), channel 16 ks:
+// the exchange of chunks is an exclusive or, so the channel is one as well, and
+// the row stays an immediate offset.  Tiles must start at multiples of a row:
+// they lie first in dynamic shared memory, in kernels without static arrays
+// (which would move its start).
+template <int D>
+__device__ __forceinline__ uint32_t piece(uint32_t lane, int r0, int ks) {
+  return (lane ^ (static_cast<uint32_t>(ks) << 5)) + static_cast<uint32_t>(r0 * D * 2);
 }
 
 // Row (0-7) of this lane's accumulator elements c[0], c[1] (c[2], c[3]: + 8),
