@@ -19,47 +19,66 @@ from typing import Optional, Sequence, Tuple
 
 import torch
 
-from . import _check, _need, _ptr, _stream, load_library
+from . import _check, _need as _needs, load_library
 
 _SIDE = contextlib.nullcontext()
 _Strides = ctypes.c_int64 * 3
 
+# A single token's call takes a few microseconds on the device, so the checks
+# here are written to cost little on the host: attributes are read once, and
+# ctypes converts plain integers.
+
 
 def _side(stream, *tensors):
     """Checks that the tensors share a device; the context in which to allocate and launch."""
-    first = tensors[0]
-    dev = first.device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got {t.device}")
-    if not first.is_cuda:
+    index = tensors[0].get_device()
+    if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on {tensors[0].device}, got {t.device}")
     if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        if stream.device.index != index:
+            raise ValueError(f"stream of {stream.device} for tensors on {tensors[0].device}")
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
         return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
+    if index != _device():
+        return torch.cuda.device(index)
     return _SIDE
+
+
+def _device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _stream() -> int:
+    """The current stream of the current device, as the library takes it."""
+    return torch._C._cuda_getCurrentRawStream(_device())
+
+
+def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _need(t: torch.Tensor, name: str, dtype, dims: int):
+    if not (t.dtype == dtype and t.dim() == dims and t.is_contiguous() and t.is_cuda):
+        _needs(t, name, dtype, dims)
+
+
+def _same(t: torch.Tensor, name: str, shape, dtype):
+    if not (t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        _needs(t, name, dtype, len(shape))
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
     """An output buffer: made here, or the caller's, checked."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _same(t, name, shape, dtype)
     return t
-
-
-def _same(t: torch.Tensor, name: str, shape, dtype):
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def _scratch(workspace, nbytes: int, device):
@@ -111,14 +130,15 @@ def _view(t: torch.Tensor, name: str, shape):
     """A token-major [B, N, H, D] bf16 view: channels contiguous.  Returns (pointer, int64[3] strides)."""
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     sb, sn, sh, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
-    # the stride of a dimension of size 1 is of no account
-    B, N, H, _ = shape
-    return t.data_ptr(), _Strides(sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0)
+    if 1 in shape:                   # the stride of a dimension of size 1 is of no account
+        B, N, H, _ = shape
+        sb, sn, sh = sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0
+    return t.data_ptr(), _Strides(sb, sn, sh)
 
 
 def _overlaps(t: torch.Tensor) -> bool:
