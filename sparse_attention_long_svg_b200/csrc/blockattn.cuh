@@ -94,20 +94,20 @@ __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int
   return *count;
 }
 
-// Rows [key0, key0 + 64) of a [Nk, D] matrix to a shared tile by THREADS
+// Rows [key0, key0 + ROWS) of a [Nk, D] matrix to a shared tile by THREADS
 // threads; rows from `len` on become zeros.
-template <int D, int THREADS>
+template <int D, int THREADS, int ROWS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const __nv_bfloat16 *src, int key0, int len, int tid) {
   constexpr int COLS = D / 8, STEP = THREADS / COLS;       // STEP rows at a time
-  static_assert(STEP % 2 == 0 && kBaTile % STEP == 0, "");
+  static_assert(STEP > 0 && ROWS % STEP == 0, "");
   const int r0 = tid / COLS, c = tid % COLS;
   const __nv_bfloat16 *from = src + static_cast<int64_t>(key0 + r0) * D + 8 * c;
-  if (key0 + kBaTile <= len) {
+  if (key0 + ROWS <= len) {
 #pragma unroll
-    for (int r = 0; r < kBaTile; r += STEP) cp_async16(dst + tile_at<D>(r0 + r, c), from + r * D, 16);
+    for (int r = 0; r < ROWS; r += STEP) cp_async16(dst + tile_at<D>(r0 + r, c), from + r * D, 16);
   } else {
 #pragma unroll
-    for (int r = 0; r < kBaTile; r += STEP) {
+    for (int r = 0; r < ROWS; r += STEP) {
       const bool in = key0 + r0 + r < len;
       cp_async16(dst + tile_at<D>(r0 + r, c), in ? from + r * D : src, in ? 16u : 0u);
     }
@@ -145,23 +145,30 @@ __device__ __forceinline__ BaRow ba_row(const BlockAttnArgs &a, int head, int le
   return x;
 }
 
-// Shared memory: tiles, then bit sets, block list, its length.
+// Shared memory: rows of K and V, then bit sets, block list, its length.
 template <int D>
-__host__ __device__ inline size_t block_attn_smem(int tiles, int tokens, int nblk) {
+__host__ __device__ inline size_t block_attn_smem(int rows, int tokens, int nblk) {
   const size_t W = (nblk + 31) / 32;
-  return static_cast<size_t>(tiles) * kBaTile * D * 2 + static_cast<size_t>(tokens) * W * 4 +
+  return static_cast<size_t>(rows) * D * 2 + static_cast<size_t>(tokens) * W * 4 +
          (static_cast<size_t>(nblk) * 2 + 15) / 16 * 16 + 16;
 }
 
-// FEW = false: 4 warps x 16 rows share each K/V tile (two tiles in flight).
+// FEW = false: 4 warps x 16 rows share each tile of 64 keys (two in flight).
 // FEW = true (at most floor(16/G) queries): all warps hold the same 16 rows and
-// take every fourth tile, each through its own buffer; the CTA joins them.
-// gridDim.y splits the union's tiles; a second kernel joins the splits.
+// take every fourth tile of 32 keys, each through its own three buffers, so that
+// 128 KB and more are always on their way (HBM bound: each listed key is read
+// once); the CTA joins the warps.  gridDim.y splits the union's tiles; a second
+// kernel joins the splits.
+template <bool FEW>
+struct BaCfg {
+  static constexpr int KEYS = FEW ? 32 : kBaTile, STAGES = FEW ? 3 : 2, BUFFERS = FEW ? 4 * STAGES : STAGES;
+  static constexpr int ROWS = BUFFERS * 2 * KEYS;          // of shared memory
+};
 template <int D, bool FEW>
 __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(const BlockAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int TILE = kBaTile * D * 2, NT = D / 8;
-  constexpr int TILES = FEW ? 8 : 4;
+  using Cfg = BaCfg<FEW>;
+  constexpr int KEYS = Cfg::KEYS, TILE = KEYS * D * 2, NT = D / 8, ST = KEYS / 8;
   const int per = 16 / a.G;                       // tokens of a warp
   const int tokens = FEW ? per : 4 * per;
   const int ntiles = (a.Nq + tokens - 1) / tokens;
@@ -169,20 +176,19 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
   const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;   // long causal rows first
   const int W = (a.nblk + 31) / 32;
   const int warp = warp_id();
-  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + TILES * TILE);
+  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + Cfg::ROWS * D * 2);
   uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
-  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(TILES, tokens, a.nblk) - 16);
+  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(Cfg::ROWS, tokens, a.nblk) - 16);
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
-  const int sub = a.block / kBaTile;
-  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
-  const int each = (total + a.splits - 1) / a.splits;
-  const int u0 = min(static_cast<int>(blockIdx.y) * each, total), u1 = min(u0 + each, total);
-
+  const int sub = a.block / KEYS;
   const int tok0 = FEW ? 0 : warp * per;
   const BaRow x0 = ba_row(a, head, len, n0, tok0, frag_row());
   const BaRow x1 = ba_row(a, head, len, n0, tok0, frag_row() + 8);
   uint32_t qf[D / 16][4];
   load_rows<D>(qf, x0.row >= 0 ? a.q + x0.row * D : nullptr, x1.row >= 0 ? a.q + x1.row * D : nullptr);
+  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
+  const int each = (total + a.splits - 1) / a.splits;
+  const int u0 = min(static_cast<int>(blockIdx.y) * each, total), u1 = min(u0 + each, total);
   const __nv_bfloat16 *kh = a.k + static_cast<int64_t>(head) * a.Nk * D;
   const __nv_bfloat16 *vh = a.v + static_cast<int64_t>(head) * a.Nk * D;
 
@@ -195,56 +201,54 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
 
   const uint32_t base = smem_u32(smem);
   const int first = FEW ? u0 + warp : u0, step = FEW ? 4 : 1;
-  auto buffer = [&](int i) { return base + static_cast<uint32_t>(FEW ? warp : (i & 1)) * 2 * TILE; };
-  auto key_of = [&](int u) { return static_cast<int>(list[u / sub]) * a.block + (u % sub) * kBaTile; };
+  auto buffer = [&](int i) {
+    return base + static_cast<uint32_t>((FEW ? warp * Cfg::STAGES : 0) + i % Cfg::STAGES) * 2 * TILE;
+  };
+  auto key_of = [&](int u) { return static_cast<int>(list[u / sub]) * a.block + (u % sub) * KEYS; };
   auto fetch = [&](int i) {
     const int u = first + i * step;
     if (u < u1) {
       const int key0 = key_of(u);
-      if (FEW) {
-        load_tile<D, 32>(buffer(i), kh, key0, len, lane_id());
-        load_tile<D, 32>(buffer(i) + TILE, vh, key0, len, lane_id());
-      } else {
-        load_tile<D, kBaThreads>(buffer(i), kh, key0, len, threadIdx.x);
-        load_tile<D, kBaThreads>(buffer(i) + TILE, vh, key0, len, threadIdx.x);
-      }
+      constexpr int THREADS = FEW ? 32 : kBaThreads;
+      const int tid = threadIdx.x % THREADS;
+      load_tile<D, THREADS, KEYS>(buffer(i), kh, key0, len, tid);
+      load_tile<D, THREADS, KEYS>(buffer(i) + TILE, vh, key0, len, tid);
     }
     cp_async_commit();
   };
-  fetch(0);
+#pragma unroll
+  for (int i = 0; i < Cfg::STAGES - 1; ++i) fetch(i);
   for (int i = 0; first + i * step < u1; ++i) {
-    if (FEW) {
-      cp_async_wait<0>();
+    fetch(i + Cfg::STAGES - 1);
+    cp_async_wait<Cfg::STAGES - 1>();
+    if (FEW)
       __syncwarp();
-    } else {
-      fetch(i + 1);
-      cp_async_wait<1>();
+    else
       __syncthreads();
-    }
     const int u = first + i * step;
     const int blk = list[u / sub], key0 = key_of(u);
     const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
     const bool on1 = x1.row >= 0 && ((bits[x1.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x1.seen;
     if (__any_sync(0xffffffffu, on0 || on1)) {
       const uint32_t kt = lane_b<D>(buffer(i)), vt = lane_a<D>(buffer(i) + TILE);
-      float s[8][4];
+      float s[ST][4];
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
+      for (int t = 0; t < ST; ++t)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks)
 #pragma unroll
-        for (int t = 0; t < 8; t += 2) {
+        for (int t = 0; t < ST; t += 2) {
           uint32_t b[4];
           ldsm_x4(piece<D>(kt, 8 * t, ks), b);
           mma_bf16(s[t], qf[ks], b[0], b[1]);
           mma_bf16(s[t + 1], qf[ks], b[2], b[3]);
         }
       const int end0 = on0 ? x0.seen - key0 : 0, end1 = on1 ? x1.seen - key0 : 0;
-      if (!__all_sync(0xffffffffu, end0 >= kBaTile && end1 >= kBaTile)) {
+      if (!__all_sync(0xffffffffu, end0 >= KEYS && end1 >= KEYS)) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
+        for (int t = 0; t < ST; ++t) {
           const int c = 8 * t + frag_col();
           s[t][0] = c < end0 ? s[t][0] : -INFINITY;
           s[t][1] = c + 1 < end0 ? s[t][1] : -INFINITY;
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
       }
       float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
+      for (int t = 0; t < ST; ++t) {
         t0 = fmaxf(t0, fmaxf(s[t][0], s[t][1]));
         t1 = fmaxf(t1, fmaxf(s[t][2], s[t][3]));
       }
@@ -274,9 +278,9 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
           acc[t][3] *= f1;
         }
       }
-      uint32_t p[4][4];
+      uint32_t p[ST / 2][4];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
+      for (int t = 0; t < ST; ++t) {
         const float p0 = ex2_approx(fmaf(s[t][0], a.scale_log2, -b0)), p1 = ex2_approx(fmaf(s[t][1], a.scale_log2, -b0));
         const float p2 = ex2_approx(fmaf(s[t][2], a.scale_log2, -b1)), p3 = ex2_approx(fmaf(s[t][3], a.scale_log2, -b1));
         l0 += p0 + p1;
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
       }
       if (__all_sync(0xffffffffu, on0 && on1)) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
+        for (int ks = 0; ks < KEYS / 16; ++ks)
 #pragma unroll
           for (int t = 0; t < NT; t += 2) {
             uint32_t b[4];
@@ -305,7 +309,7 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[j][e] = acc[t + j][e];
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
+          for (int ks = 0; ks < KEYS / 16; ++ks)
 #pragma unroll
             for (int j = 0; j < 4; j += 2) {
               uint32_t b[4];
@@ -320,12 +324,10 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
         }
       }
     }
-    if (FEW) {
+    if (FEW)
       __syncwarp();
-      fetch(i + 1);
-    } else {
+    else
       __syncthreads();
-    }
   }
   cp_async_wait<0>();
   l0 = quad_sum(l0);
@@ -459,7 +461,7 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
   const int warp = warp_id();
   uint32_t *bits = reinterpret_cast<uint32_t *>(smem + 4 * TILE);
   uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
-  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(4, tokens, a.nblk) - 16);
+  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(4 * kBaTile, tokens, a.nblk) - 16);
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const int sub = a.block / kBaTile;
   const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
@@ -500,8 +502,8 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
   auto fetch = [&](int u) {
     if (u < total) {
       const uint32_t buf = base + static_cast<uint32_t>(u & 1) * 2 * TILE;
-      load_tile<D, kBaThreads>(buf, kh, key_of(u), len, threadIdx.x);
-      load_tile<D, kBaThreads>(buf + TILE, vh, key_of(u), len, threadIdx.x);
+      load_tile<D, kBaThreads, kBaTile>(buf, kh, key_of(u), len, threadIdx.x);
+      load_tile<D, kBaThreads, kBaTile>(buf + TILE, vh, key_of(u), len, threadIdx.x);
     }
     cp_async_commit();
   };

@@ -659,7 +659,7 @@ __device__ __forceinline__ int cta_sum(int v, int (&part)[2][kSelDecodeThreads /
 }
 
 template <int D>
-__global__ void __launch_bounds__(kSelDecodeThreads) block_select_decode_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kSelDecodeThreads, 1) block_select_decode_kernel(const SelectArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   double *exact = reinterpret_cast<double *>(smem);               // [nblk]
   float *scores = reinterpret_cast<float *>(exact + a.nblk);      // [nblk]
@@ -702,8 +702,12 @@ __global__ void __launch_bounds__(kSelDecodeThreads) block_select_decode_kernel(
     qa = row_sum<D>(norm_part(qa, z));
   }
   __syncthreads();
+  // A group of GT lanes takes U = GT/2 blocks at a time, which makes GT sums (U
+  // scores, U squared norms): they are added over the lanes by halving, so that
+  // lane c ends with the c-th sum.
   uint32_t biggest = 0;
-  constexpr int PER = kSelDecodeThreads / GT, U = 4;              // blocks of a round, rounds in flight
+  constexpr int PER = kSelDecodeThreads / GT, U = GT / 2;
+#pragma unroll 2
   for (int j0 = 0; j0 < r.may; j0 += PER * U) {
     float4 v[U][4];
 #pragma unroll
@@ -711,24 +715,41 @@ __global__ void __launch_bounds__(kSelDecodeThreads) block_select_decode_kernel(
       const int j = j0 + u * PER + threadIdx.x / GT;
       const float4 *src = reinterpret_cast<const float4 *>(a.mean + (static_cast<int64_t>(head) * a.nblk + j) * D);
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        v[u][e] = j < r.may ? __ldg(src + (e < 2 ? 2 * c + e : 2 * GT + 2 * c + e - 2)) : make_float4(0, 0, 0, 0);
+      for (int e = 0; e < 4; ++e) {
+        v[u][e] = make_float4(0, 0, 0, 0);
+        if (j < r.may) v[u][e] = __ldg(src + (e < 2 ? 2 * c + e : 2 * GT + 2 * c + e - 2));
+      }
     }
+    float sum[GT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * PER + threadIdx.x / GT;
-      float s = 0.f, nn = 0.f;
-      bool none = true;
+      float2 s = make_float2(0.f, 0.f), nn = s;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        none = none && v[u][e].x == 0.f && v[u][e].y == 0.f && v[u][e].z == 0.f && v[u][e].w == 0.f;
-        s += v[u][e].x * qs[4 * e] + v[u][e].y * qs[4 * e + 1] + v[u][e].z * qs[4 * e + 2] + v[u][e].w * qs[4 * e + 3];
-        nn += v[u][e].x * v[u][e].x + v[u][e].y * v[u][e].y + v[u][e].z * v[u][e].z + v[u][e].w * v[u][e].w;
+        const float2 lo = make_float2(v[u][e].x, v[u][e].y), hi = make_float2(v[u][e].z, v[u][e].w);
+        s = fma_f32x2(lo, make_float2(qs[4 * e], qs[4 * e + 1]), s);
+        s = fma_f32x2(hi, make_float2(qs[4 * e + 2], qs[4 * e + 3]), s);
+        nn = fma_f32x2(lo, lo, nn);
+        nn = fma_f32x2(hi, hi, nn);
       }
-      s = row_sum<D>(s);
-      nn = row_sum<D>(none ? 0.f : nn < kNormFloor ? kNormFloor : nn);
-      if (j < r.may && c == 0) scores[j] = s;
-      biggest = max(biggest, nn <= 3.4e38f ? __float_as_uint(nn) : 0x7F800000u);
+      sum[u] = s.x + s.y;
+      sum[U + u] = nn.x + nn.y;
+    }
+#pragma unroll
+    for (int half = GT / 2; half > 0; half >>= 1) {
+      const bool upper = (c & half) != 0;
+#pragma unroll
+      for (int i = 0; i < half; ++i) {
+        const float give = upper ? sum[i] : sum[half + i], keep = upper ? sum[half + i] : sum[i];
+        sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, half);
+      }
+    }
+    const int j = j0 + (c % U) * PER + threadIdx.x / GT;
+    if (c < U) {
+      if (j < r.may) scores[j] = sum[0];
+    } else {
+      // not below the floor (see norm_part), and NaN or infinity: all exact
+      biggest = max(biggest, sum[0] <= 3.4e38f ? __float_as_uint(fmaxf(sum[0], kNormFloor)) : 0x7F800000u);
     }
   }
   biggest = __reduce_max_sync(0xffffffffu, biggest);

@@ -1026,8 +1026,8 @@ struct BlockAttnPlan {
   bool few;
   int tokens, tiles, splits;
 };
-// Few CTAs: the union of a tile's blocks is split until the GPU is full, at
-// least 4 tiles to a part.
+// Few CTAs: the union of a tile's blocks is split into what one wave of CTAs
+// holds, at least 4 x 64 keys to a part.
 BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int block) {
   BlockAttnPlan p;
   const int per = 16 / (BHq / BHk);
@@ -1037,8 +1037,8 @@ BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int 
   const int64_t ctas = static_cast<int64_t>(BHk) * p.tiles;
   const int64_t listed = static_cast<int64_t>(Nq < p.tokens ? Nq : p.tokens) * topk;
   const int64_t keys = (listed < nblk ? listed : nblk) * (block / kBaTile);
-  const int64_t target = (p.few ? 1ll : 2ll) * num_sms();
-  int64_t s = (target + ctas - 1) / ctas;
+  const int64_t wave = (p.few ? 1ll : 3ll) * num_sms();
+  int64_t s = wave / ctas;
   if (s > (keys + 3) / 4) s = (keys + 3) / 4;
   if (s > kBaMaxSplits) s = kBaMaxSplits;
   p.splits = static_cast<int>(s < 1 ? 1 : s);
@@ -1242,11 +1242,11 @@ svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, 
     return launch_status("block_attn_kernel");
   };
   if (D == 128)
-    st = p.few ? go(block_attn_kernel<128, true>, block_attn_smem<128>(8, p.tokens, nblk))
-               : go(block_attn_kernel<128, false>, block_attn_smem<128>(4, p.tokens, nblk));
+    st = p.few ? go(block_attn_kernel<128, true>, block_attn_smem<128>(BaCfg<true>::ROWS, p.tokens, nblk))
+               : go(block_attn_kernel<128, false>, block_attn_smem<128>(BaCfg<false>::ROWS, p.tokens, nblk));
   else
-    st = p.few ? go(block_attn_kernel<64, true>, block_attn_smem<64>(8, p.tokens, nblk))
-               : go(block_attn_kernel<64, false>, block_attn_smem<64>(4, p.tokens, nblk));
+    st = p.few ? go(block_attn_kernel<64, true>, block_attn_smem<64>(BaCfg<true>::ROWS, p.tokens, nblk))
+               : go(block_attn_kernel<64, false>, block_attn_smem<64>(BaCfg<false>::ROWS, p.tokens, nblk));
   if (st != SVG_OK || p.splits == 1) return st;
   const unsigned join = static_cast<unsigned>((static_cast<int64_t>(BHq) * Nq + 3) / 4);
   if (D == 128)
@@ -1327,9 +1327,9 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
     return launch_status("block_attn gradient kernels");
   };
   if (D == 128)
-    return go(block_attn_dq_kernel<128>, block_attn_smem<128>(4, tokens, nblk), block_attn_dkv_kernel<128>,
+    return go(block_attn_dq_kernel<128>, block_attn_smem<128>(4 * kBaTile, tokens, nblk), block_attn_dkv_kernel<128>,
               block_attn_dkv_smem<128>(w.item_tokens), block_attn_dkv_join_kernel<128>);
-  return go(block_attn_dq_kernel<64>, block_attn_smem<64>(4, tokens, nblk), block_attn_dkv_kernel<64>,
+  return go(block_attn_dq_kernel<64>, block_attn_smem<64>(4 * kBaTile, tokens, nblk), block_attn_dkv_kernel<64>,
             block_attn_dkv_smem<64>(w.item_tokens), block_attn_dkv_join_kernel<64>);
 }
 
