@@ -26,40 +26,82 @@ __device__ __forceinline__ int seq_len(const int32_t *kv_len, int b, int Nk) {
   return kv_len ? min(max(kv_len[b], 0), Nk) : Nk;
 }
 
-// One CTA per (head, block): 256 threads = D/8 16-byte columns x row slots.
-// HBM bound: reads the keys once.
+// bf16 to fp64 at the two halves of a word.  The low one goes through the
+// conversion unit, which would take as long as the memory for all; the high one
+// is put together by integer operations: its bits, moved to a double's sign,
+// exponent and mantissa, are the value times 2^-896 (subnormals included, but
+// not infinities and NaN).
+__device__ __forceinline__ double low_bf16(uint32_t x) { return static_cast<double>(__uint_as_float(x << 16)); }
+__device__ __forceinline__ double high_bf16_scaled(uint32_t x) {
+  return __hiloint2double(static_cast<int>(((x & 0x7FFF0000u) >> 3) | (x & 0x80000000u)), 0);
+}
+
+// One warp per block: D/8 lanes hold the 16-byte columns of a row, the warp 2
+// (D = 64: 4) rows at a time with 8 loads in flight, so that neither shared
+// memory nor a barrier is needed.  HBM bound: reads the keys once.
+constexpr int kMeanThreads = 128;
+
 template <int D>
-__global__ void __launch_bounds__(256) block_mean_kernel(const __nv_bfloat16 *k, int Nk, int block, int nblk,
-                                                         const int32_t *kv_len, int heads_per_seq, int fresh,
-                                                         int per_head, float *mean) {
-  constexpr int COLS = D / 8, SLOTS = 256 / COLS;
-  __shared__ double sums[SLOTS][D];
-  const int head = blockIdx.x / per_head;
+__global__ void __launch_bounds__(kMeanThreads) block_mean_kernel(const __nv_bfloat16 *k, int Nk, int block, int nblk,
+                                                                  const int32_t *kv_len, int heads_per_seq, int fresh,
+                                                                  int per_head, int blocks, float *mean) {
+  constexpr int COLS = D / 8, SLOTS = 32 / COLS, U = 8;
+  const int i = blockIdx.x * (kMeanThreads / 32) + warp_id();
+  if (i >= blocks) return;
+  const int head = i / per_head;
   const int len = seq_len(kv_len, head / heads_per_seq, Nk);
-  const int blk = blockIdx.x % per_head + (fresh > 0 ? max(0, len - fresh) / block : 0);
+  const int blk = i % per_head + (fresh > 0 ? max(0, len - fresh) / block : 0);
   if (blk >= nblk) return;
   const int rows = min(max(len - blk * block, 0), block);
   if (fresh > 0 && rows == 0) return;
-  const int col = threadIdx.x % COLS, slot = threadIdx.x / COLS;
+  const int col = lane_id() % COLS, slot = lane_id() / COLS;
   const __nv_bfloat16 *src = k + (static_cast<int64_t>(head) * Nk + static_cast<int64_t>(blk) * block) * D + 8 * col;
   double acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0;
-#pragma unroll 4
-  for (int r = slot; r < rows; r += SLOTS) {
-    float f[8];
-    unpack8(__ldg(reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * D)), f);
+  for (int e = 0; e < 8; ++e) acc[e] = 0.0;
+  uint32_t big = 0;
+  for (int r0 = 0; r0 < rows; r0 += U * SLOTS) {
+    uint4 v[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] += static_cast<double>(f[i]);
+    for (int u = 0; u < U; ++u)        // without conditions, so that all are in flight
+      v[u] = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(min(r0 + u * SLOTS + slot, rows - 1)) * D));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = r0 + u * SLOTS + slot < rows;
+      const uint32_t w[4] = {in ? v[u].x : 0u, in ? v[u].y : 0u, in ? v[u].z : 0u, in ? v[u].w : 0u};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[2 * e] += low_bf16(w[e]);
+        acc[2 * e + 1] += high_bf16_scaled(w[e]);
+        big = max(big, w[e] & 0x7FFFFFFFu);
+      }
+    }
+  }
+  if (__any_sync(0xffffffffu, big >= 0x7F800000u)) {       // infinities or NaN: the high halves again
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[2 * e + 1] = 0.0;
+    for (int r = slot; r < rows; r += SLOTS) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + static_cast<int64_t>(r) * D));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[2 * e + 1] += static_cast<double>(__uint_as_float(w[e] & 0xFFFF0000u));
+    }
+  } else {
+    const double unscale = __hiloint2double((1023 + 896) << 20, 0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[2 * e + 1] *= unscale;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[slot][8 * col + i] = acc[i];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    double s = 0.0;
-    for (int i = 0; i < SLOTS; ++i) s += sums[i][threadIdx.x];
-    mean[(static_cast<int64_t>(head) * nblk + blk) * D + threadIdx.x] =
-        rows > 0 ? static_cast<float>(s / static_cast<double>(rows)) : 0.f;
+  for (int o = COLS; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+  if (slot == 0) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = rows > 0 ? static_cast<float>(acc[e] / static_cast<double>(rows)) : 0.f;
+    float4 *dst = reinterpret_cast<float4 *>(mean + (static_cast<int64_t>(head) * nblk + blk) * D + 8 * col);
+    dst[0] = make_float4(f[0], f[1], f[2], f[3]);
+    dst[1] = make_float4(f[4], f[5], f[6], f[7]);
   }
 }
 

@@ -153,13 +153,10 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
   for (int i = 0; i < p.hpt; i += U) {
     uint4 va[U], vb[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = h0 + i + u;
-      va[u] = vb[u] = make_uint4(0, 0, 0, 0);
-      if (ok && h < h1) {
-        va[u] = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t]));
-        vb[u] = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t] + D / 2));
-      }
+    for (int u = 0; u < U; ++u) {      // without conditions, so that all are in flight
+      const int h = max(min(h0 + i + u, h1 - 1), 0);
+      va[u] = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t]));
+      vb[u] = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t] + D / 2));
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -184,19 +181,22 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
       }
       if (store && h < h1) {
         __nv_bfloat16 *yr = y + h * p.cap[t] * D;
-        *reinterpret_cast<uint4 *>(yr) = va[u];
-        *reinterpret_cast<uint4 *>(yr + D / 2) = vb[u];
+        *reinterpret_cast<uint4 *>(yr) = ok ? va[u] : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(yr + D / 2) = ok ? vb[u] : make_uint4(0, 0, 0, 0);
       }
     }
   }
 }
 
 // grid (token tiles, head chunks): one CTA stays with one chunk, so that its
-// threads sum dw of one tensor.  Sums run in fp32 over a thread's rows (a few
-// hundred) and in fp64 over the partial sums.
+// threads sum dw of one tensor.  The next head's rows are on their way while a
+// head is computed.  Sums run in fp32 over a thread's rows (a hundred or so)
+// and a CTA's groups, and in fp64 over the CTAs.
+constexpr int kRopeBackThreads = 128;
+
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_backward_kernel(const RopeArgs p) {
-  constexpr int GT = D / 16, GROUPS = kRopeThreads / GT;
+__global__ void __launch_bounds__(kRopeBackThreads, 5) qk_norm_rope_backward_kernel(const RopeArgs p) {
+  constexpr int GT = D / 16, GROUPS = kRopeBackThreads / GT;
   __shared__ float sums[GROUPS][D];
   const int c = threadIdx.x % GT, grp = threadIdx.x / GT;
   const int64_t tokens = static_cast<int64_t>(p.B) * p.N;
@@ -218,6 +218,22 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_backward_kernel(con
       record_error(SVG_ERR_DEVICE_CHECK, SVG_SITE_ROPE_RANGE);
       ok = false;
     }
+    const __nv_bfloat16 *x = t == 2 ? nullptr : p.x[t] + b * p.xb[t] + n * p.xn[t] + 8 * c;
+    // rows that do not count are read all the same, at a row that exists
+    const int64_t from = ok ? row : 0;
+    const __nv_bfloat16 *dy = p.dy[t] + (static_cast<int64_t>(b) * p.heads[t] * p.cap[t] + from) * D + 8 * c;
+    __nv_bfloat16 *dx = p.dx[t] + b * p.db[t] + n * p.dn[t] + 8 * c;
+    uint4 ga, gb, xa, xb;
+    auto load = [&](int next) {
+      const int h = min(next, h1 - 1);
+      ga = __ldcs(reinterpret_cast<const uint4 *>(dy + h * p.cap[t] * D));
+      gb = __ldcs(reinterpret_cast<const uint4 *>(dy + h * p.cap[t] * D + D / 2));
+      if (t != 2) {
+        xa = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t]));
+        xb = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t] + D / 2));
+      }
+    };
+    load(h0);
     float cs[8], sn[8];
     const bool turn = ok && t != 2 && p.cos != nullptr;
     if (turn) {
@@ -225,52 +241,46 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_backward_kernel(con
 #pragma unroll
       for (int j = 0; j < 8; ++j) sn[j] = -sn[j];          // the transposed rotation
     }
-    const __nv_bfloat16 *x = t == 2 ? nullptr : p.x[t] + b * p.xb[t] + n * p.xn[t] + 8 * c;
-    const __nv_bfloat16 *dy = p.dy[t] + (static_cast<int64_t>(b) * p.heads[t] * p.cap[t] + row) * D + 8 * c;
-    __nv_bfloat16 *dx = p.dx[t] + b * p.db[t] + n * p.dn[t] + 8 * c;
-#pragma unroll 2
     for (int h = h0; h < h1; ++h) {
-      uint4 ga = make_uint4(0, 0, 0, 0), gb = ga, xa = ga, xb = ga;
-      if (ok) {
-        ga = __ldcs(reinterpret_cast<const uint4 *>(dy + h * p.cap[t] * D));
-        gb = __ldcs(reinterpret_cast<const uint4 *>(dy + h * p.cap[t] * D + D / 2));
-        if (t != 2) {
-          xa = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t]));
-          xb = __ldcs(reinterpret_cast<const uint4 *>(x + h * p.xh[t] + D / 2));
+      if (t == 2) {                                         // one tensor per CTA: no divergence
+        const uint4 va = ga, vb = gb;
+        load(h + 1);
+        if (live) {
+          *reinterpret_cast<uint4 *>(dx + h * p.dh[t]) = ok ? va : make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(dx + h * p.dh[t] + D / 2) = ok ? vb : make_uint4(0, 0, 0, 0);
         }
+        continue;
       }
-      if (t != 2) {                                         // one tensor per CTA: no divergence
-        float u[8], v[8], a[8], bb[8];
-        unpack8(ga, u);
-        unpack8(gb, v);
-        unpack8(xa, a);
-        unpack8(xb, bb);
-        if (turn) rope_turn<INTER>(u, v, cs, sn);
-        float ss = 0.f, gx = 0.f;
+      float u[8], v[8], a[8], bb[8];
+      unpack8(ga, u);
+      unpack8(gb, v);
+      unpack8(xa, a);
+      unpack8(xb, bb);
+      load(h + 1);
+      if (turn) rope_turn<INTER>(u, v, cs, sn);
+      float ss = 0.f, gx = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          ss += a[j] * a[j] + bb[j] * bb[j];
-          gx += u[j] * wa[j] * a[j] + v[j] * wb[j] * bb[j];
-        }
-        ss = row_sum<D>(ss);
-        gx = row_sum<D>(gx);
-        const float r = rsqrtf(ss * (1.f / D) + p.eps);
-        const float m = gx * r * (1.f / D);                 // mean of g n
+      for (int j = 0; j < 8; ++j) {
+        ss += a[j] * a[j] + bb[j] * bb[j];
+        gx += u[j] * wa[j] * a[j] + v[j] * wb[j] * bb[j];
+      }
+      ss = row_sum<D>(ss);
+      gx = row_sum<D>(gx);
+      const float r = rsqrtf(ss * (1.f / D) + p.eps);
+      const float m = gx * r * (1.f / D);                   // mean of g n
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float na = a[j] * r, nb = bb[j] * r;
+      for (int j = 0; j < 8; ++j) {
+        const float na = a[j] * r, nb = bb[j] * r;
+        if (ok) {
           da[j] += u[j] * na;
           db[j] += v[j] * nb;
-          u[j] = r * (u[j] * wa[j] - na * m);
-          v[j] = r * (v[j] * wb[j] - nb * m);
         }
-        ga = pack8(u);
-        gb = pack8(v);
-        if (!ok) ga = gb = make_uint4(0, 0, 0, 0);
+        u[j] = r * (u[j] * wa[j] - na * m);
+        v[j] = r * (v[j] * wb[j] - nb * m);
       }
       if (live) {
-        *reinterpret_cast<uint4 *>(dx + h * p.dh[t]) = ga;
-        *reinterpret_cast<uint4 *>(dx + h * p.dh[t] + D / 2) = gb;
+        *reinterpret_cast<uint4 *>(dx + h * p.dh[t]) = ok ? pack8(u) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(dx + h * p.dh[t] + D / 2) = ok ? pack8(v) : make_uint4(0, 0, 0, 0);
       }
     }
   }
@@ -283,30 +293,33 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_backward_kernel(con
   __syncthreads();
   if (threadIdx.x < D) {
     float s = 0.f;
+#pragma unroll
     for (int g = 0; g < GROUPS; ++g) s += sums[g][threadIdx.x];
     p.partial[(static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x) * D + threadIdx.x] = s;
   }
 }
 
-// dw[t] = sum of its partial rows: grid (D/8, 2), 32 row slices x 8 channels
+// dw[t] = sum of its partial rows: grid (D/8, 2), 128 row slices x 8 channels
 // per CTA, added in a fixed order.
 template <int D>
-__global__ void __launch_bounds__(256) rope_dw_kernel(const float *partial, int rows_q, int rows_k, float *dw_q,
-                                                      float *dw_k) {
-  __shared__ double part[32][8];
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float *partial, int rows_q, int rows_k, float *dw_q,
+                                                       float *dw_k) {
+  __shared__ double part[128][8];
   float *dw = blockIdx.y == 0 ? dw_q : dw_k;
   if (dw == nullptr) return;
   const int rows = blockIdx.y == 0 ? rows_q : rows_k;
   const float *src = partial + (blockIdx.y == 0 ? 0 : static_cast<int64_t>(rows_q) * D);
-  const int col = blockIdx.x * 8 + threadIdx.x % 8, slice = threadIdx.x / 8;
+  const int ch = threadIdx.x % 8, col = blockIdx.x * 8 + ch, slice = threadIdx.x / 8;
   double s = 0.0;
-  for (int r = slice; r < rows; r += 32) s += static_cast<double>(src[static_cast<int64_t>(r) * D + col]);
-  part[slice][threadIdx.x % 8] = s;
+#pragma unroll 8
+  for (int r = slice; r < rows; r += 128) s += static_cast<double>(src[static_cast<int64_t>(r) * D + col]);
+  part[slice][ch] = s;
   __syncthreads();
-  if (threadIdx.x < 8) {
-    for (int i = 1; i < 32; ++i) s += part[i][threadIdx.x];
-    dw[col] = static_cast<float>(s);
+  for (int n = 64; n > 0; n >>= 1) {
+    if (slice < n) part[slice][ch] += part[slice + n][ch];
+    __syncthreads();
   }
+  if (slice == 0) dw[col] = static_cast<float>(part[0][ch]);
 }
 
 }  // namespace svg

@@ -811,8 +811,6 @@ extern "C" svg_status svg_sparse_attn_noalloc(const void *qp, const void *kp, co
 
 // ------------------------------------------------------------------ Q/K norm with rotation
 namespace {
-constexpr int kRopeBackwardTiles = 4 * 148;    // CTAs of the gradient (bounds its partial sums)
-
 // Strides of a token-major view must keep rows on 16-byte boundaries.
 bool rope_strides_ok(const int64_t *s) { return s && s[0] % 8 == 0 && s[1] % 8 == 0 && s[2] % 8 == 0; }
 
@@ -841,7 +839,7 @@ svg_status rope_args(RopeArgs &a, const void *const *x, const int64_t *const *xs
     a.cap[t] = t == 0 ? N : cap;
     if (x[t] == nullptr) a.heads[t] = 0;
     if (a.heads[t] == 0) continue;
-    if (!aligned(x[t], 16) || !rope_strides_ok(xs[t])) return SVG_ERR_INVALID_ARG;
+    if (!aligned(x[t], 16) || !rope_strides_ok(xs[t]) || a.cap[t] < 1) return SVG_ERR_INVALID_ARG;
     a.x[t] = static_cast<const __nv_bfloat16 *>(x[t]);
     a.xb[t] = xs[t][0];
     a.xn[t] = xs[t][1];
@@ -855,13 +853,16 @@ void rope_chunks(RopeArgs &a, int hpt) {
   for (int t = 0; t < 3; ++t) a.chunks[t] = (a.heads[t] + hpt - 1) / hpt;
 }
 
-// Heads of a CTA's chunk in the gradient, and its token tiles.
-int rope_backward_heads(int Hq, int Hk) { return Hq + Hk > 16 ? 8 : 4; }
+// Heads of a CTA's chunk in the gradient.
+constexpr int kRopeBackwardHeads = 8;
+// Token tiles: each CTA goes over as many as leave about 4 waves of CTAs (5 per
+// SM), all the same number; this also bounds the partial sums of dw.
 int rope_backward_tiles(int B, int N, int D, int chunks) {
-  const int64_t groups = kRopeThreads / (D / 16);
-  const int64_t tiles = (static_cast<int64_t>(B) * N + groups - 1) / groups;
-  const int64_t most = (kRopeBackwardTiles + chunks - 1) / chunks;
-  return static_cast<int>(tiles < most ? tiles : most);
+  const int64_t groups = kRopeBackThreads / (D / 16);
+  const int64_t all = (static_cast<int64_t>(B) * N + groups - 1) / groups;
+  const int64_t most = 4ll * 5 * num_sms();
+  const int64_t each = (all * chunks + most - 1) / most;
+  return static_cast<int>((all + each - 1) / each);
 }
 }  // namespace
 
@@ -912,8 +913,8 @@ svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void 
 
 size_t svg_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, int D) {
   if (B <= 0 || N <= 0 || Hq <= 0 || Hk < 0 || (D != 64 && D != 128)) return 0;
-  const int hpt = rope_backward_heads(Hq, Hk);
-  const int cq = (Hq + hpt - 1) / hpt, ck = (Hk + hpt - 1) / hpt;
+  const int cq = (Hq + kRopeBackwardHeads - 1) / kRopeBackwardHeads;
+  const int ck = (Hk + kRopeBackwardHeads - 1) / kRopeBackwardHeads;
   return align256(static_cast<size_t>(cq + ck) * rope_backward_tiles(B, N, D, cq + ck) * D * sizeof(float));
 }
 
@@ -949,13 +950,13 @@ svg_status svg_qk_norm_rope_backward(const void *dq_out, const void *dk_out, con
   if (cos && !start && P < N) return SVG_ERR_INVALID_ARG;
   if (!aligned(ws, 256)) return SVG_ERR_INVALID_ARG;
   if (ws_bytes < svg_qk_norm_rope_backward_workspace_size(B, N, Hq, Hk, D)) return SVG_ERR_WORKSPACE;
-  rope_chunks(a, rope_backward_heads(Hq, Hk));
+  rope_chunks(a, kRopeBackwardHeads);
   a.partial = static_cast<float *>(ws);
   const int tiles = rope_backward_tiles(B, N, D, (Hq + a.hpt - 1) / a.hpt + (Hk + a.hpt - 1) / a.hpt);
   const dim3 grid(tiles, a.chunks[0] + a.chunks[1] + a.chunks[2]);
   if (grid.y > 65535u) return SVG_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto kernel) { kernel<<<grid, kRopeThreads, 0, s>>>(a); };
+  auto go = [&](auto kernel) { kernel<<<grid, kRopeBackThreads, 0, s>>>(a); };
   if (D == 128)
     interleaved ? go(qk_norm_rope_backward_kernel<128, true>) : go(qk_norm_rope_backward_kernel<128, false>);
   else
@@ -964,9 +965,9 @@ svg_status svg_qk_norm_rope_backward(const void *dq_out, const void *dk_out, con
   if (st != SVG_OK || (!dw_q && !dw_k)) return st;
   const int rows_q = a.chunks[0] * tiles, rows_k = a.chunks[1] * tiles;
   if (D == 128)
-    rope_dw_kernel<128><<<dim3(16, 2), 256, 0, s>>>(a.partial, rows_q, rows_k, dw_q, dw_k);
+    rope_dw_kernel<128><<<dim3(16, 2), 1024, 0, s>>>(a.partial, rows_q, rows_k, dw_q, dw_k);
   else
-    rope_dw_kernel<64><<<dim3(8, 2), 256, 0, s>>>(a.partial, rows_q, rows_k, dw_q, dw_k);
+    rope_dw_kernel<64><<<dim3(8, 2), 1024, 0, s>>>(a.partial, rows_q, rows_k, dw_q, dw_k);
   return launch_status("rope_dw_kernel");
 }
 
@@ -1112,11 +1113,12 @@ svg_status svg_block_mean(const void *k, int BHk, int B, int Nk, int D, int bloc
   if (per * BHk >= (1ll << 31)) return SVG_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const __nv_bfloat16 *kb = static_cast<const __nv_bfloat16 *>(k);
-  const unsigned grid = static_cast<unsigned>(per * BHk);
-  if (D == 128)
-    block_mean_kernel<128><<<grid, 256, 0, s>>>(kb, Nk, block, nblk, kv_len, BHk / B, fresh, static_cast<int>(per), mean);
-  else
-    block_mean_kernel<64><<<grid, 256, 0, s>>>(kb, Nk, block, nblk, kv_len, BHk / B, fresh, static_cast<int>(per), mean);
+  const int blocks = static_cast<int>(per * BHk);
+  const unsigned grid = static_cast<unsigned>((blocks + kMeanThreads / 32 - 1) / (kMeanThreads / 32));
+  auto go = [&](auto kernel) {
+    kernel<<<grid, kMeanThreads, 0, s>>>(kb, Nk, block, nblk, kv_len, BHk / B, fresh, static_cast<int>(per), blocks, mean);
+  };
+  D == 128 ? go(block_mean_kernel<128>) : go(block_mean_kernel<64>);
   return launch_status("block_mean_kernel");
 }
 

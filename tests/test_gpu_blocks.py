@@ -209,6 +209,20 @@ def test_block_means_are_exact(Nk, block, D):
     assert torch.equal(svg.block_mean(k, block)[:Hk], mean[:Hk])
 
 
+def test_block_means_of_subnormals_infinities_and_nan():
+    k = bf(44, 1, 320, 64)
+    bits = torch.randint(-32768, 32768, (64, 64), generator=torch.Generator().manual_seed(45), dtype=torch.int32)
+    bits = torch.where((bits & 0x7F80) == 0x7F80, bits & ~0x4000, bits)
+    k[0, :64] = ((bits & 0x807F) | 0x0080).to(torch.int16).view(BF).cuda()        # the smallest normal values
+    k[0, 64:128] = (bits & 0x807F).to(torch.int16).view(BF).cuda()                # subnormals and zeros
+    k[0, 130, 3], k[0, 130, 4] = float("inf"), -float("inf")
+    k[0, 200, 7], k[0, 201, 7] = float("inf"), -float("inf")
+    k[0, 260, 9], k[0, 260, 10] = float("nan"), float("nan")
+    got = svg.block_mean(k, 64).cpu().numpy()
+    want = bo.block_means(f64(k), 64, [320])
+    assert np.array_equal(got, want, equal_nan=True), np.argwhere(~((got == want) | (np.isnan(got) & np.isnan(want))))[:5]
+
+
 @pytest.mark.parametrize("new", [1, 3, 65, 1000])
 def test_block_means_of_the_newest_keys(new):
     B, Hk, Nk, D = 4, 2, 520, 128
