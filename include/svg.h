@@ -447,7 +447,8 @@ typedef enum svg_error_site {
   SVG_SITE_KMEANS_EPI = 8,      /* k-means assign: epilogue warps */
   SVG_SITE_KMEANS_RANGE = 9,    /* k-means update: cluster id outside [0, C) */
   SVG_SITE_KMEANS_DRAIN = 10,   /* k-means assign: waiting for copies in flight after an abort */
-  SVG_SITE_ROPE_RANGE = 11      /* Q/K norm with rotation: position beyond the table or the buffer */
+  SVG_SITE_ROPE_RANGE = 11,     /* Q/K norm with rotation: position beyond the table or the buffer */
+  SVG_SITE_BLOCK_ATTN = 12      /* attention over chosen blocks, or its gradient: any wait */
 } svg_error_site;
 
 /* Same as svg_get_error (synchronises, returns and clears the error word),

@@ -151,7 +151,7 @@ def get_error(stream=None) -> int:
 
 ERROR_SITES = {0: "none", 1: "attention producer", 2: "attention MMA issuer", 3: "attention softmax",
                4: "attention drain", 5: "attention planning", 6: "permute range", 7: "k-means MMA issuer",
-               8: "k-means epilogue", 9: "k-means range", 10: "k-means drain", 11: "rotation range"}
+               8: "k-means epilogue", 9: "k-means range", 10: "k-means drain", 11: "rotation range", 12: "block attention"}
 
 
 def get_error_detail(stream=None) -> Tuple[int, str, int]:

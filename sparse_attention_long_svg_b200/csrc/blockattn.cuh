@@ -44,6 +44,7 @@ struct BlockAttnArgs {
   int BHk, G, heads_per_seq, Nq, Nk, nblk, block, topk, causal, splits;
   int item_tokens;
   float scale, scale_log2;
+  uint64_t wait_ns;
 };
 
 // Keys the query n sees.
@@ -56,10 +57,10 @@ __device__ __forceinline__ int query_seen(const BlockAttnArgs &a, int len, int n
 // outside the sequence and blocks without a visible key are passed over.
 __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int len, int n0, int tokens, int W,
                                            uint32_t *bits, uint16_t *list, int *count) {
-  for (int i = threadIdx.x; i < tokens * W; i += kBaThreads) bits[i] = 0;
+  for (int i = threadIdx.x; i < tokens * W; i += blockDim.x) bits[i] = 0;
   __syncthreads();
   const int32_t *sel = a.sel + (static_cast<int64_t>(head) * a.Nq + n0) * a.topk;
-  for (int i = threadIdx.x; i < tokens * a.topk; i += kBaThreads) {
+  for (int i = threadIdx.x; i < tokens * a.topk; i += blockDim.x) {
     const int tok = i / a.topk;
     if (n0 + tok >= a.Nq) break;
     const int j = sel[i];
@@ -153,37 +154,31 @@ __host__ __device__ inline size_t block_attn_smem(int rows, int tokens, int nblk
          (static_cast<size_t>(nblk) * 2 + 15) / 16 * 16 + 16;
 }
 
-// FEW = false: 4 warps x 16 rows share each tile of 64 keys (two in flight).
-// FEW = true (at most floor(16/G) queries): all warps hold the same 16 rows and
-// take every fourth tile of 32 keys, each through its own three buffers, so that
-// 128 KB and more are always on their way (HBM bound: each listed key is read
-// once); the CTA joins the warps.  gridDim.y splits the union's tiles; a second
-// kernel joins the splits.
-template <bool FEW>
-struct BaCfg {
-  static constexpr int KEYS = FEW ? 32 : kBaTile, STAGES = FEW ? 3 : 2, BUFFERS = FEW ? 4 * STAGES : STAGES;
-  static constexpr int ROWS = BUFFERS * 2 * KEYS;          // of shared memory
-};
-template <int D, bool FEW>
-__global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(const BlockAttnArgs a) {
+// Few queries (at most floor(16/G), single tokens among them): all warps hold
+// the same 16 rows and take every fourth tile of 32 keys, each through its own
+// three buffers, so that 128 KB and more are always on their way (HBM bound:
+// each listed key is read once); the CTA joins the warps.  gridDim.y splits the
+// union's tiles; a second kernel joins the splits.
+constexpr int kFewKeys = 32, kFewStages = 3, kFewRows = 4 * kFewStages * 2 * kFewKeys;   // rows of shared memory
+
+template <int D>
+__global__ void __launch_bounds__(kBaThreads, 1) block_attn_few_kernel(const BlockAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  using Cfg = BaCfg<FEW>;
-  constexpr int KEYS = Cfg::KEYS, TILE = KEYS * D * 2, NT = D / 8, ST = KEYS / 8;
+  constexpr int KEYS = kFewKeys, STAGES = kFewStages, TILE = KEYS * D * 2, NT = D / 8, ST = KEYS / 8;
   const int per = 16 / a.G;                       // tokens of a warp
-  const int tokens = FEW ? per : 4 * per;
+  const int tokens = per;
   const int ntiles = (a.Nq + tokens - 1) / tokens;
   const int head = blockIdx.x % a.BHk;
   const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;   // long causal rows first
   const int W = (a.nblk + 31) / 32;
   const int warp = warp_id();
-  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + Cfg::ROWS * D * 2);
+  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + kFewRows * D * 2);
   uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
-  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(Cfg::ROWS, tokens, a.nblk) - 16);
+  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(kFewRows, tokens, a.nblk) - 16);
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const int sub = a.block / KEYS;
-  const int tok0 = FEW ? 0 : warp * per;
-  const BaRow x0 = ba_row(a, head, len, n0, tok0, frag_row());
-  const BaRow x1 = ba_row(a, head, len, n0, tok0, frag_row() + 8);
+  const BaRow x0 = ba_row(a, head, len, n0, 0, frag_row());
+  const BaRow x1 = ba_row(a, head, len, n0, 0, frag_row() + 8);
   uint32_t qf[D / 16][4];
   load_rows<D>(qf, x0.row >= 0 ? a.q + x0.row * D : nullptr, x1.row >= 0 ? a.q + x1.row * D : nullptr);
   const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
@@ -200,31 +195,26 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
   const uint32_t base = smem_u32(smem);
-  const int first = FEW ? u0 + warp : u0, step = FEW ? 4 : 1;
+  const int first = u0 + warp, step = 4;
   auto buffer = [&](int i) {
-    return base + static_cast<uint32_t>((FEW ? warp * Cfg::STAGES : 0) + i % Cfg::STAGES) * 2 * TILE;
+    return base + static_cast<uint32_t>(warp * STAGES + i % STAGES) * 2 * TILE;
   };
   auto key_of = [&](int u) { return static_cast<int>(list[u / sub]) * a.block + (u % sub) * KEYS; };
   auto fetch = [&](int i) {
     const int u = first + i * step;
     if (u < u1) {
       const int key0 = key_of(u);
-      constexpr int THREADS = FEW ? 32 : kBaThreads;
-      const int tid = threadIdx.x % THREADS;
-      load_tile<D, THREADS, KEYS>(buffer(i), kh, key0, len, tid);
-      load_tile<D, THREADS, KEYS>(buffer(i) + TILE, vh, key0, len, tid);
+      load_tile<D, 32, KEYS>(buffer(i), kh, key0, len, lane_id());
+      load_tile<D, 32, KEYS>(buffer(i) + TILE, vh, key0, len, lane_id());
     }
     cp_async_commit();
   };
 #pragma unroll
-  for (int i = 0; i < Cfg::STAGES - 1; ++i) fetch(i);
+  for (int i = 0; i < STAGES - 1; ++i) fetch(i);
   for (int i = 0; first + i * step < u1; ++i) {
-    fetch(i + Cfg::STAGES - 1);
-    cp_async_wait<Cfg::STAGES - 1>();
-    if (FEW)
-      __syncwarp();
-    else
-      __syncthreads();
+    fetch(i + STAGES - 1);
+    cp_async_wait<STAGES - 1>();
+    __syncwarp();
     const int u = first + i * step;
     const int blk = list[u / sub], key0 = key_of(u);
     const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
@@ -324,92 +314,60 @@ __global__ void __launch_bounds__(kBaThreads, FEW ? 1 : 3) block_attn_kernel(con
         }
       }
     }
-    if (FEW)
-      __syncwarp();
-    else
-      __syncthreads();
+    __syncwarp();
   }
   cp_async_wait<0>();
   l0 = quad_sum(l0);
   l1 = quad_sum(l1);
 
-  if (FEW) {
-    // join the four warps' sums: [warp][16 rows][D] and maxima / sums behind
-    __syncthreads();
-    float *so = reinterpret_cast<float *>(smem);
-    float *sm = so + 4 * 16 * D, *sl = sm + 64;
-    const int r0 = frag_row();
+  // join the four warps' sums: [warp][16 rows][D] and maxima / sums behind
+  __syncthreads();
+  float *so = reinterpret_cast<float *>(smem);
+  float *sm = so + 4 * 16 * D, *sl = sm + 64;
+  const int r0 = frag_row();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int c = 8 * t + frag_col();
-      *reinterpret_cast<float2 *>(so + (warp * 16 + r0) * D + c) = make_float2(acc[t][0], acc[t][1]);
-      *reinterpret_cast<float2 *>(so + (warp * 16 + r0 + 8) * D + c) = make_float2(acc[t][2], acc[t][3]);
-    }
-    if ((lane_id() & 3) == 0) {
-      sm[warp * 16 + r0] = m0;
-      sm[warp * 16 + r0 + 8] = m1;
-      sl[warp * 16 + r0] = l0;
-      sl[warp * 16 + r0 + 8] = l1;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * D / 2; i += kBaThreads) {
-      const int r = i / (D / 2), c = (i % (D / 2)) * 2;
-      const BaRow x = ba_row(a, head, len, n0, 0, r);
-      if (x.row < 0) continue;
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) m = fmaxf(m, sm[w * 16 + r]);
-      const float b = m == -INFINITY ? 0.f : m;
-      float l = 0.f, y0 = 0.f, y1 = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = ex2_approx(sm[w * 16 + r] - b);
-        const float2 v = *reinterpret_cast<const float2 *>(so + (w * 16 + r) * D + c);
-        l += f * sl[w * 16 + r];
-        // a warp without a visible key holds zeros
-        y0 += f * v.x;
-        y1 += f * v.y;
-      }
-      const bool none = m == -INFINITY && l == 0.f;
-      const float inv = none ? 0.f : 1.f / l;
-      y0 *= inv;
-      y1 *= inv;
-      const float lse2 = none ? -INFINITY : m + log2f(l);
-      if (a.splits > 1) {
-        const int64_t pr = static_cast<int64_t>(blockIdx.y) * a.BHk * a.G * a.Nq + x.row;
-        *reinterpret_cast<float2 *>(a.part_o + pr * D + c) = make_float2(y0, y1);
-        if (c == 0) a.part_lse[pr] = lse2;
-      } else {
-        *reinterpret_cast<uint32_t *>(a.o + x.row * D + c) = pack_bf16(y0, y1);
-        if (c == 0 && a.lse) a.lse[x.row] = lse2 * 0.69314718055994531f;
-      }
-    }
-    return;
+  for (int t = 0; t < NT; ++t) {
+    const int c = 8 * t + frag_col();
+    *reinterpret_cast<float2 *>(so + (warp * 16 + r0) * D + c) = make_float2(acc[t][0], acc[t][1]);
+    *reinterpret_cast<float2 *>(so + (warp * 16 + r0 + 8) * D + c) = make_float2(acc[t][2], acc[t][3]);
   }
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const BaRow &x = half ? x1 : x0;
-    const float m = half ? m1 : m0, l = half ? l1 : l0;
+  if ((lane_id() & 3) == 0) {
+    sm[warp * 16 + r0] = m0;
+    sm[warp * 16 + r0 + 8] = m1;
+    sl[warp * 16 + r0] = l0;
+    sl[warp * 16 + r0 + 8] = l1;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * D / 2; i += kBaThreads) {
+    const int r = i / (D / 2), c = (i % (D / 2)) * 2;
+    const BaRow x = ba_row(a, head, len, n0, 0, r);
     if (x.row < 0) continue;
+    float m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, sm[w * 16 + r]);
+    const float b = m == -INFINITY ? 0.f : m;
+    float l = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = ex2_approx(sm[w * 16 + r] - b);
+      const float2 v = *reinterpret_cast<const float2 *>(so + (w * 16 + r) * D + c);
+      l += f * sl[w * 16 + r];
+      // a warp without a visible key holds zeros
+      y0 += f * v.x;
+      y1 += f * v.y;
+    }
     const bool none = m == -INFINITY && l == 0.f;
     const float inv = none ? 0.f : 1.f / l;
+    y0 *= inv;
+    y1 *= inv;
     const float lse2 = none ? -INFINITY : m + log2f(l);
-    const bool split = a.splits > 1;
-    const int64_t pr = static_cast<int64_t>(blockIdx.y) * a.BHk * a.G * a.Nq + x.row;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float y0 = acc[t][2 * half] * inv, y1 = acc[t][2 * half + 1] * inv;
-      const int c = 8 * t + frag_col();
-      if (split)
-        *reinterpret_cast<float2 *>(a.part_o + pr * D + c) = make_float2(y0, y1);
-      else
-        *reinterpret_cast<uint32_t *>(a.o + x.row * D + c) = pack_bf16(y0, y1);
-    }
-    if ((lane_id() & 3) == 0) {
-      if (split)
-        a.part_lse[pr] = lse2;
-      else if (a.lse)
-        a.lse[x.row] = lse2 * 0.69314718055994531f;
+    if (a.splits > 1) {
+      const int64_t pr = static_cast<int64_t>(blockIdx.y) * a.BHk * a.G * a.Nq + x.row;
+      *reinterpret_cast<float2 *>(a.part_o + pr * D + c) = make_float2(y0, y1);
+      if (c == 0) a.part_lse[pr] = lse2;
+    } else {
+      *reinterpret_cast<uint32_t *>(a.o + x.row * D + c) = pack_bf16(y0, y1);
+      if (c == 0 && a.lse) a.lse[x.row] = lse2 * 0.69314718055994531f;
     }
   }
 }

@@ -702,7 +702,7 @@ __device__ __forceinline__ int cta_sum(int v, int (&part)[2][kSelDecodeThreads /
 
 template <int D>
 __global__ void __launch_bounds__(kSelDecodeThreads, 1) block_select_decode_kernel(const SelectArgs a) {
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   double *exact = reinterpret_cast<double *>(smem);               // [nblk]
   float *scores = reinterpret_cast<float *>(exact + a.nblk);      // [nblk]
   int *who = reinterpret_cast<int *>(scores + a.nblk);            // [nblk]

@@ -9,6 +9,7 @@
 
 #include "attn.cuh"
 #include "blockattn.cuh"
+#include "blockattn_tc.cuh"
 #include "blocksel.cuh"
 #include "common.cuh"
 #include "dynrad.cuh"
@@ -1033,12 +1034,12 @@ BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int 
   BlockAttnPlan p;
   const int per = 16 / (BHq / BHk);
   p.few = Nq <= per;
-  p.tokens = p.few ? per : 4 * per;
+  p.tokens = p.few ? per : kTcRows / (BHq / BHk);
   p.tiles = (Nq + p.tokens - 1) / p.tokens;
   const int64_t ctas = static_cast<int64_t>(BHk) * p.tiles;
   const int64_t listed = static_cast<int64_t>(Nq < p.tokens ? Nq : p.tokens) * topk;
   const int64_t keys = (listed < nblk ? listed : nblk) * (block / kBaTile);
-  const int64_t wave = (p.few ? 1ll : 3ll) * num_sms();
+  const int64_t wave = (p.few ? 1ll : 2ll) * num_sms();
   int64_t s = wave / ctas;
   if (s > (keys + 3) / 4) s = (keys + 3) / 4;
   if (s > kBaMaxSplits) s = kBaMaxSplits;
@@ -1097,6 +1098,7 @@ void block_attn_args(BlockAttnArgs &a, const void *q, const void *k, const void 
   a.splits = 1;
   a.scale = scale > 0.f ? scale : 1.f / std::sqrt(static_cast<float>(D));
   a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.wait_ns = g_wait_ns;
 }
 }  // namespace
 
@@ -1238,17 +1240,17 @@ svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, 
   if (ctas >= (1ll << 31)) return SVG_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(ctas), p.splits);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  auto go = [&](auto kernel, size_t smem) {
+  auto go = [&](auto kernel, int threads, size_t smem) {
     if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
-    kernel<<<grid, kBaThreads, smem, s>>>(a);
+    kernel<<<grid, threads, smem, s>>>(a);
     return launch_status("block_attn_kernel");
   };
   if (D == 128)
-    st = p.few ? go(block_attn_kernel<128, true>, block_attn_smem<128>(BaCfg<true>::ROWS, p.tokens, nblk))
-               : go(block_attn_kernel<128, false>, block_attn_smem<128>(BaCfg<false>::ROWS, p.tokens, nblk));
+    st = p.few ? go(block_attn_few_kernel<128>, kBaThreads, block_attn_smem<128>(kFewRows, p.tokens, nblk))
+               : go(block_attn_tc_kernel<128>, kTcThreads, tc_smem<128>(1, p.tokens, nblk));
   else
-    st = p.few ? go(block_attn_kernel<64, true>, block_attn_smem<64>(BaCfg<true>::ROWS, p.tokens, nblk))
-               : go(block_attn_kernel<64, false>, block_attn_smem<64>(BaCfg<false>::ROWS, p.tokens, nblk));
+    st = p.few ? go(block_attn_few_kernel<64>, kBaThreads, block_attn_smem<64>(kFewRows, p.tokens, nblk))
+               : go(block_attn_tc_kernel<64>, kTcThreads, tc_smem<64>(1, p.tokens, nblk));
   if (st != SVG_OK || p.splits == 1) return st;
   const unsigned join = static_cast<unsigned>((static_cast<int64_t>(BHq) * Nq + 3) / 4);
   if (D == 128)
