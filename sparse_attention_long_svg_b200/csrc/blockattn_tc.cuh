@@ -13,7 +13,7 @@
 
 namespace svg {
 
-constexpr int kTcRows = 128, kTcThreads = 224, kTcLoaders = 64;
+constexpr int kTcRows = 128, kTcThreads = 224;
 
 // Byte offset of 16-byte chunk c of row r in a 128-byte-swizzled tile of ROWS
 // rows: 64-channel halves of 128-byte rows, chunks exchanged by the row's low bits.
@@ -22,12 +22,12 @@ __device__ __forceinline__ uint32_t tc_at(int r, int c) {
   return static_cast<uint32_t>((c >> 3) * ROWS * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
-// Rows [key0, key0 + 64) of a [Nk, D] matrix by the loader threads; rows from
-// `len` on become zeros.
+// Rows [key0, key0 + 64) of a [Nk, D] matrix by one warp; rows from `len` on
+// become zeros.
 template <int D>
-__device__ __forceinline__ void tc_load_tile(uint32_t dst, const __nv_bfloat16 *src, int key0, int len, int tid) {
-  constexpr int COLS = D / 8, STEP = kTcLoaders / COLS;
-  const int r0 = tid / COLS, c = tid % COLS;
+__device__ __forceinline__ void tc_load_tile(uint32_t dst, const __nv_bfloat16 *src, int key0, int len) {
+  constexpr int COLS = D / 8, STEP = 32 / COLS;
+  const int r0 = lane_id() / COLS, c = lane_id() % COLS;
   const __nv_bfloat16 *from = src + static_cast<int64_t>(key0 + r0) * D + 8 * c;
   if (key0 + kBaTile <= len) {
 #pragma unroll
@@ -55,8 +55,8 @@ __device__ __forceinline__ void tc_load_rows(uint8_t *dst, const __nv_bfloat16 *
   }
 }
 
-struct TcBars {
-  uint64_t full[2], empty[2], s_full[2], p_full[2], done, drain;
+struct TcBars {                       // at most 192 bytes
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], done, drain;
   uint32_t tmem;
   int count;
 };
@@ -77,7 +77,7 @@ __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t parity, uin
 template <int D>
 __host__ __device__ inline size_t tc_smem(int operands, int tokens, int nblk) {
   const size_t W = (nblk + 31) / 32;
-  return static_cast<size_t>(operands) * kTcRows * D * 2 + 4ull * kBaTile * D * 2 + 128 +
+  return static_cast<size_t>(operands) * kTcRows * D * 2 + 4ull * kBaTile * D * 2 + 192 +
          static_cast<size_t>(tokens) * W * 4 + static_cast<size_t>(nblk) * 2 + 16;
 }
 
@@ -98,9 +98,11 @@ __device__ __forceinline__ float dot_rows(const __nv_bfloat16 *a, const __nv_bfl
 struct TcUnion {
   const uint16_t *list;
   const uint32_t *bits;
-  int u0, u1, sub, block, W;
-  __device__ __forceinline__ int block_of(int u) const { return list[u / sub]; }
-  __device__ __forceinline__ int key(int u) const { return block_of(u) * block + (u % sub) * kBaTile; }
+  int u0, u1, shift, W;                // a block has 2^shift tiles of 64 keys
+  __device__ __forceinline__ int block_of(int u) const { return list[u >> shift]; }
+  __device__ __forceinline__ int key(int u) const {
+    return ((block_of(u) << shift) + (u & ((1 << shift) - 1))) * kBaTile;
+  }
   __device__ __forceinline__ bool listed(int tok, int u) const {
     const int j = block_of(u);
     return (bits[tok * W + (j >> 5)] >> (j & 31)) & 1u;
@@ -158,7 +160,8 @@ __device__ __noinline__ void row_again(const TcUnion &un, const __nv_bfloat16 *q
 }
 
 // Warps 0-3: softmax (thread = row = TMEM lane); warp 4: its lane 0 issues the
-// matrix products; warps 5, 6: K/V loads.  Two score buffers in TMEM; a row's
+// matrix products; warp 5 loads K, warp 6 V (two stages each: a K tile is free
+// again before the weights of its scores are).  Two score buffers in TMEM; a row's
 // weights replace its scores there (bf16, the A operand of the product with V).
 //   S(t+1) is issued before P(t) V, so the tensor cores run while the softmax
 //   of the other buffer (or of the SM's other CTA) does.
@@ -174,13 +177,13 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   constexpr float kRaise = 8.f;
   uint8_t *sKV = smem + Q_BYTES;                    // [stage][K, V]
   TcBars *B = reinterpret_cast<TcBars *>(sKV + 4 * KV);
-  uint32_t *bits = reinterpret_cast<uint32_t *>(sKV + 4 * KV + 128);
+  uint32_t *bits = reinterpret_cast<uint32_t *>(sKV + 4 * KV + 192);
   const int tokens = kTcRows / a.G;
   const int W = (a.nblk + 31) / 32;
   uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
   const int ntiles = (a.Nq + tokens - 1) / tokens;
-  const int head = blockIdx.x % a.BHk;
-  const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;   // long causal rows first
+  const int head = blockIdx.x / ntiles;             // one head after the other: its K and V stay in L2
+  const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x % ntiles)) * tokens;
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const int warp = warp_id(), lane = lane_id();
   const uint64_t ns = a.wait_ns;
@@ -196,8 +199,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B->full[i], kTcLoaders);
-      mbar_init(&B->empty[i], 1);
+      mbar_init(&B->k_full[i], 32);
+      mbar_init(&B->k_empty[i], 1);
+      mbar_init(&B->v_full[i], 32);
+      mbar_init(&B->v_empty[i], 1);
       mbar_init(&B->s_full[i], 1);
       mbar_init(&B->p_full[i], 128);
     }
@@ -210,11 +215,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   TcUnion un;
   un.list = list;
   un.bits = bits;
-  un.sub = a.block / kBaTile;
-  un.block = a.block;
+  un.shift = a.block == kBaTile ? 0 : 1;
   un.W = W;
   tc_fence_before();
-  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, &B->count) * un.sub;
+  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, &B->count) << un.shift;
   tc_fence_after();
   const uint32_t tmem = B->tmem;
   const int each = (total + a.splits - 1) / a.splits;
@@ -225,16 +229,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   const __nv_bfloat16 *vh = a.v + static_cast<int64_t>(head) * a.Nk * D;
 
   if (warp >= 5) {
-    // ---------------------------------------------------------------- loads
-    const int tid = threadIdx.x - 5 * 32;
+    // ---------------------------------------------------------------- loads: K, V
+    const bool is_v = warp == 6;
+    uint64_t *full = is_v ? B->v_full : B->k_full, *empty = is_v ? B->v_empty : B->k_empty;
     for (int t = 0; t < steps; ++t) {
       const int st = t & 1;
-      if (t >= 2 && !tc_warp_wait(&B->empty[st], ((t >> 1) - 1) & 1, ns)) break;
-      const int key0 = un.key(un.u0 + t);
-      const uint32_t dst = smem_u32(sKV) + static_cast<uint32_t>(st) * 2 * KV;
-      tc_load_tile<D>(dst, kh, key0, len, tid);
-      tc_load_tile<D>(dst + KV, vh, key0, len, tid);
-      cp_async_arrive(&B->full[st]);
+      if (t >= 2 && !tc_warp_wait(&empty[st], ((t >> 1) - 1) & 1, ns)) break;
+      tc_load_tile<D>(smem_u32(sKV) + static_cast<uint32_t>(2 * st + is_v) * KV, is_v ? vh : kh, un.key(un.u0 + t), len);
+      cp_async_arrive(&full[st]);
     }
     cp_async_commit();
     cp_async_wait<0>();
@@ -246,13 +248,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
       const SmemDesc vd = make_desc_sw128(smem_u32(sKV) + KV, kBaTile * 128, 1024);
       auto issue_s = [&](int t) {
         const int st = t & 1;
-        if (!tc_wait(&B->full[st], (t >> 1) & 1, ns)) return false;
+        if (!tc_wait(&B->k_full[st], (t >> 1) & 1, ns)) return false;
         fence_proxy_async_smem();                   // cp.async writes -> tensor-core reads
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
         mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, qd,
                                                                 SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
         mma_commit(&B->s_full[st]);
+        mma_commit(&B->k_empty[st]);
         return true;
       };
       bool ok = steps == 0 || issue_s(0);
@@ -260,7 +263,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
         const int st = t & 1;
         // its score buffer held P(t-1), whose product was issued before
         if (t + 1 < steps && !issue_s(t + 1)) break;
-        if (!tc_wait(&B->p_full[st], (t >> 1) & 1, ns)) break;
+        if (!tc_wait(&B->v_full[st], (t >> 1) & 1, ns) || !tc_wait(&B->p_full[st], (t >> 1) & 1, ns)) break;
+        fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
 #pragma unroll
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
           mma_bf16_ts(tmem, tmem + TM_S + st * kBaTile + 8 * k,
                       (static_cast<uint64_t>(vd.hi) << 32) | (vd.lo + off + ((k * 2048) >> 4)), IDESC_PV,
                       t > 0 || k > 0 ? 1u : 0u);
-        mma_commit(&B->empty[st]);
+        mma_commit(&B->v_empty[st]);
         mma_commit(&B->done);
       }
       mma_commit(&B->drain);                        // all retired before TMEM is released
@@ -293,6 +297,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
         break;
       }
       tc_fence_after();
+      if (!__any_sync(0xffffffffu, end > 0)) {      // none of the warp's rows lists the block
+        float p[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) p[c] = 0.f;
+        tmem_st32(s_at, p);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&B->p_full[st]);
+        continue;
+      }
       float s[64];
       tmem_ld64_sync(s_at, s);
       if (__any_sync(0xffffffffu, end > 0 && end < kBaTile)) {
