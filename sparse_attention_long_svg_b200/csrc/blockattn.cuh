@@ -52,47 +52,65 @@ __device__ __forceinline__ int query_seen(const BlockAttnArgs &a, int len, int n
   return a.causal ? min(len - a.Nq + n + 1, len) : len;
 }
 
-// Bit sets of the blocks of `tokens` tokens from n0 on (one per token, W words
-// each, at `bits`), their union as an ascending list; returns its length.  Ids
-// outside the sequence and blocks without a visible key are passed over.
+// Bit sets of the blocks of `tokens` tokens from n0 on (word w of token t at
+// bits[w * tokens + t], W words), their union as an ascending list; returns its
+// length.  Ids outside the sequence and blocks without a visible key are passed
+// over.  Called by all threads; uni: W words of scratch.
 __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int len, int n0, int tokens, int W,
-                                           uint32_t *bits, uint16_t *list, int *count) {
-  for (int i = threadIdx.x; i < tokens * W; i += blockDim.x) bits[i] = 0;
-  __syncthreads();
+                                           uint32_t *bits, uint32_t *uni, uint16_t *list, int *count) {
+  constexpr int U = 8;                              // ids in flight per thread
+  const int threads = blockDim.x, tid = threadIdx.x, lane = lane_id();
+  for (int i = tid; i < tokens * W; i += threads) bits[i] = 0;
   const int32_t *sel = a.sel + (static_cast<int64_t>(head) * a.Nq + n0) * a.topk;
-  for (int i = threadIdx.x; i < tokens * a.topk; i += blockDim.x) {
-    const int tok = i / a.topk;
-    if (n0 + tok >= a.Nq) break;
-    const int j = sel[i];
-    if (j >= 0 && j < a.nblk && static_cast<int64_t>(j) * a.block < query_seen(a, len, n0 + tok))
-      atomicOr(&bits[tok * W + (j >> 5)], 1u << (j & 31));
+  const int ids = min(tokens, a.Nq - n0) * a.topk;
+  __syncthreads();
+  for (int i0 = tid; i0 < ids; i0 += U * threads) {
+    int j[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) j[u] = __ldg(sel + min(i0 + u * threads, ids - 1));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * threads;
+      if (i >= ids) break;
+      const int tok = i / a.topk;
+      if (j[u] >= 0 && j[u] < a.nblk && static_cast<int64_t>(j[u]) * a.block < query_seen(a, len, n0 + tok))
+        atomicOr(&bits[(j[u] >> 5) * tokens + tok], 1u << (j[u] & 31));
+    }
+  }
+  __syncthreads();
+  for (int w = warp_id(); w < W; w += threads / 32) {
+    uint32_t u = 0;
+    for (int t = lane; t < tokens; t += 32) u |= bits[w * tokens + t];
+    u = __reduce_or_sync(0xffffffffu, u);
+    if (lane == 0) uni[w] = u;
   }
   __syncthreads();
   if (warp_id() == 0) {
     int at = 0;
     for (int w0 = 0; w0 < W; w0 += 32) {
-      const int w = w0 + lane_id();
-      uint32_t u = 0;
-      if (w < W)
-        for (int t = 0; t < tokens; ++t) u |= bits[t * W + w];
+      const int w = w0 + lane;
+      uint32_t u = w < W ? uni[w] : 0u;
       int pre = __popc(u);
+      const int own = pre;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, pre, o);
-        if (static_cast<int>(lane_id()) >= o) pre += x;
+        if (lane >= o) pre += x;
       }
       const int all = __shfl_sync(0xffffffffu, pre, 31);
-      int p = at + pre - __popc(u);
-      while (u) {
-        list[p++] = static_cast<uint16_t>(w * 32 + __ffs(u) - 1);
-        u &= u - 1;
-      }
+      for (int p = at + pre - own; u; u &= u - 1) list[p++] = static_cast<uint16_t>(w * 32 + __ffs(u) - 1);
       at += all;
     }
-    if (lane_id() == 0) *count = at;
+    if (lane == 0) *count = at;
   }
   __syncthreads();
   return *count;
+}
+
+// Bytes of the bit sets, their union and its list.
+__host__ __device__ inline size_t mark_bytes(int tokens, int nblk) {
+  const size_t W = (nblk + 31) / 32;
+  return (static_cast<size_t>(tokens) + 1) * W * 4 + static_cast<size_t>(nblk) * 2;
 }
 
 // Rows [key0, key0 + ROWS) of a [Nk, D] matrix to a shared tile by THREADS
@@ -146,12 +164,10 @@ __device__ __forceinline__ BaRow ba_row(const BlockAttnArgs &a, int head, int le
   return x;
 }
 
-// Shared memory: rows of K and V, then bit sets, block list, its length.
+// Shared memory: rows of K and V, then the list's length, bit sets, list.
 template <int D>
 __host__ __device__ inline size_t block_attn_smem(int rows, int tokens, int nblk) {
-  const size_t W = (nblk + 31) / 32;
-  return static_cast<size_t>(rows) * D * 2 + static_cast<size_t>(tokens) * W * 4 +
-         (static_cast<size_t>(nblk) * 2 + 15) / 16 * 16 + 16;
+  return static_cast<size_t>(rows) * D * 2 + 16 + mark_bytes(tokens, nblk);
 }
 
 // Few queries (at most floor(16/G), single tokens among them): all warps hold
@@ -172,16 +188,16 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_few_kernel(const Blo
   const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;   // long causal rows first
   const int W = (a.nblk + 31) / 32;
   const int warp = warp_id();
-  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + kFewRows * D * 2);
-  uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
-  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(kFewRows, tokens, a.nblk) - 16);
+  int *count = reinterpret_cast<int *>(smem + kFewRows * D * 2);
+  uint32_t *bits = reinterpret_cast<uint32_t *>(count + 4), *uni = bits + tokens * W;
+  uint16_t *list = reinterpret_cast<uint16_t *>(uni + W);
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const int sub = a.block / KEYS;
   const BaRow x0 = ba_row(a, head, len, n0, 0, frag_row());
   const BaRow x1 = ba_row(a, head, len, n0, 0, frag_row() + 8);
   uint32_t qf[D / 16][4];
   load_rows<D>(qf, x0.row >= 0 ? a.q + x0.row * D : nullptr, x1.row >= 0 ? a.q + x1.row * D : nullptr);
-  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
+  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, uni, list, count) * sub;
   const int each = (total + a.splits - 1) / a.splits;
   const int u0 = min(static_cast<int>(blockIdx.y) * each, total), u1 = min(u0 + each, total);
   const __nv_bfloat16 *kh = a.k + static_cast<int64_t>(head) * a.Nk * D;
@@ -217,8 +233,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_few_kernel(const Blo
     __syncwarp();
     const int u = first + i * step;
     const int blk = list[u / sub], key0 = key_of(u);
-    const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
-    const bool on1 = x1.row >= 0 && ((bits[x1.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x1.seen;
+    const bool on0 = x0.row >= 0 && ((bits[(blk >> 5) * tokens + x0.tok] >> (blk & 31)) & 1u) && key0 < x0.seen;
+    const bool on1 = x1.row >= 0 && ((bits[(blk >> 5) * tokens + x1.tok] >> (blk & 31)) & 1u) && key0 < x1.seen;
     if (__any_sync(0xffffffffu, on0 || on1)) {
       const uint32_t kt = lane_b<D>(buffer(i)), vt = lane_a<D>(buffer(i) + TILE);
       float s[ST][4];
@@ -417,12 +433,12 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
   const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;
   const int W = (a.nblk + 31) / 32;
   const int warp = warp_id();
-  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + 4 * TILE);
-  uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
-  int *count = reinterpret_cast<int *>(smem + block_attn_smem<D>(4 * kBaTile, tokens, a.nblk) - 16);
+  int *count = reinterpret_cast<int *>(smem + 4 * TILE);
+  uint32_t *bits = reinterpret_cast<uint32_t *>(count + 4), *uni = bits + tokens * W;
+  uint16_t *list = reinterpret_cast<uint16_t *>(uni + W);
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const int sub = a.block / kBaTile;
-  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, count) * sub;
+  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, uni, list, count) * sub;
 
   const BaRow x0 = ba_row(a, head, len, n0, warp * per, frag_row());
   const BaRow x1 = ba_row(a, head, len, n0, warp * per, frag_row() + 8);
@@ -471,8 +487,8 @@ __global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAt
     cp_async_wait<1>();
     __syncthreads();
     const int blk = list[u / sub], key0 = key_of(u);
-    const bool on0 = x0.row >= 0 && ((bits[x0.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x0.seen;
-    const bool on1 = x1.row >= 0 && ((bits[x1.tok * W + (blk >> 5)] >> (blk & 31)) & 1u) && key0 < x1.seen;
+    const bool on0 = x0.row >= 0 && ((bits[(blk >> 5) * tokens + x0.tok] >> (blk & 31)) & 1u) && key0 < x0.seen;
+    const bool on1 = x1.row >= 0 && ((bits[(blk >> 5) * tokens + x1.tok] >> (blk & 31)) & 1u) && key0 < x1.seen;
     if (__any_sync(0xffffffffu, on0 || on1)) {
       const uint32_t tile = base + static_cast<uint32_t>(u & 1) * 2 * TILE;
       const uint32_t kt = lane_b<D>(tile), vt = kt + TILE, kx = lane_a<D>(tile);

@@ -42,16 +42,14 @@ __device__ __forceinline__ void tc_load_tile(uint32_t dst, const __nv_bfloat16 *
 }
 
 // A 128-row operand tile (row r of the CTA = row(r) of a [rows, D] matrix, -1:
-// zeros) by all threads, through registers.
+// zeros) by all threads.
 template <int D, typename F>
-__device__ __forceinline__ void tc_load_rows(uint8_t *dst, const __nv_bfloat16 *src, F row) {
+__device__ __forceinline__ void tc_load_rows(uint32_t dst, const __nv_bfloat16 *src, F row) {
   constexpr int COLS = D / 8;
   for (int i = threadIdx.x; i < kTcRows * COLS; i += kTcThreads) {
     const int r = i / COLS, c = i % COLS;
     const int64_t at = row(r);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (at >= 0) v = __ldg(reinterpret_cast<const uint4 *>(src + at * D + 8 * c));
-    *reinterpret_cast<uint4 *>(dst + tc_at<kTcRows>(r, c)) = v;
+    cp_async16(dst + tc_at<kTcRows>(r, c), src + (at >= 0 ? at * D + 8 * c : 0), at >= 0 ? 16u : 0u);
   }
 }
 
@@ -76,9 +74,7 @@ __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t parity, uin
 // stages of K and V, barriers, bit sets, block list.
 template <int D>
 __host__ __device__ inline size_t tc_smem(int operands, int tokens, int nblk) {
-  const size_t W = (nblk + 31) / 32;
-  return static_cast<size_t>(operands) * kTcRows * D * 2 + 4ull * kBaTile * D * 2 + 192 +
-         static_cast<size_t>(tokens) * W * 4 + static_cast<size_t>(nblk) * 2 + 16;
+  return static_cast<size_t>(operands) * kTcRows * D * 2 + 4ull * kBaTile * D * 2 + 192 + mark_bytes(tokens, nblk);
 }
 
 __device__ __forceinline__ float dot_rows(const __nv_bfloat16 *a, const __nv_bfloat16 *b, int D) {
@@ -98,14 +94,14 @@ __device__ __forceinline__ float dot_rows(const __nv_bfloat16 *a, const __nv_bfl
 struct TcUnion {
   const uint16_t *list;
   const uint32_t *bits;
-  int u0, u1, shift, W;                // a block has 2^shift tiles of 64 keys
+  int u0, u1, shift, tokens;           // a block has 2^shift tiles of 64 keys
   __device__ __forceinline__ int block_of(int u) const { return list[u >> shift]; }
   __device__ __forceinline__ int key(int u) const {
     return ((block_of(u) << shift) + (u & ((1 << shift) - 1))) * kBaTile;
   }
   __device__ __forceinline__ bool listed(int tok, int u) const {
     const int j = block_of(u);
-    return (bits[tok * W + (j >> 5)] >> (j & 31)) & 1u;
+    return (bits[(j >> 5) * tokens + tok] >> (j & 31)) & 1u;
   }
 };
 
@@ -180,7 +176,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   uint32_t *bits = reinterpret_cast<uint32_t *>(sKV + 4 * KV + 192);
   const int tokens = kTcRows / a.G;
   const int W = (a.nblk + 31) / 32;
-  uint16_t *list = reinterpret_cast<uint16_t *>(bits + tokens * W);
+  uint32_t *uni = bits + tokens * W;
+  uint16_t *list = reinterpret_cast<uint16_t *>(uni + W);
   const int ntiles = (a.Nq + tokens - 1) / tokens;
   const int head = blockIdx.x / ntiles;             // one head after the other: its K and V stay in L2
   const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x % ntiles)) * tokens;
@@ -210,16 +207,19 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
     mbar_init(&B->drain, 1);
     fence_mbar_init();
   }
-  tc_load_rows<D>(smem, a.q, row_of);
-  fence_proxy_async_smem();
+  tc_load_rows<D>(smem_u32(smem), a.q, row_of);
+  cp_async_commit();
   TcUnion un;
   un.list = list;
   un.bits = bits;
   un.shift = a.block == kBaTile ? 0 : 1;
-  un.W = W;
+  un.tokens = tokens;
   tc_fence_before();
-  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, list, &B->count) << un.shift;
+  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, uni, list, &B->count) << un.shift;
   tc_fence_after();
+  cp_async_wait<0>();
+  fence_proxy_async_smem();
+  __syncthreads();
   const uint32_t tmem = B->tmem;
   const int each = (total + a.splits - 1) / a.splits;
   un.u0 = min(static_cast<int>(blockIdx.y) * each, total);
