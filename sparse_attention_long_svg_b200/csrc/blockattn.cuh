@@ -42,7 +42,7 @@ struct BlockAttnArgs {
   int32_t *items;                      // key tile of every work item
   float *part_kv;                      // [slot][2][64][D]
   int BHk, G, heads_per_seq, Nq, Nk, nblk, block, topk, causal, splits;
-  int item_tokens;
+  int item_tokens, tile_tokens;
   float scale, scale_log2;
   uint64_t wait_ns;
 };
@@ -421,147 +421,6 @@ __global__ void __launch_bounds__(128) block_attn_join_kernel(const BlockAttnArg
 }
 
 // ------------------------------------------------------------------ gradient
-// dQ (and delta for the second kernel): the forward kernel's walk with two more
-// products per tile, 32 keys at a time to stay in registers.
-template <int D>
-__global__ void __launch_bounds__(kBaThreads) block_attn_dq_kernel(const BlockAttnArgs a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int TILE = kBaTile * D * 2, NT = D / 8;
-  const int per = 16 / a.G, tokens = 4 * per;
-  const int ntiles = (a.Nq + tokens - 1) / tokens;
-  const int head = blockIdx.x % a.BHk;
-  const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x / a.BHk)) * tokens;
-  const int W = (a.nblk + 31) / 32;
-  const int warp = warp_id();
-  int *count = reinterpret_cast<int *>(smem + 4 * TILE);
-  uint32_t *bits = reinterpret_cast<uint32_t *>(count + 4), *uni = bits + tokens * W;
-  uint16_t *list = reinterpret_cast<uint16_t *>(uni + W);
-  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
-  const int sub = a.block / kBaTile;
-  const int total = mark_blocks(a, head, len, n0, tokens, W, bits, uni, list, count) * sub;
-
-  const BaRow x0 = ba_row(a, head, len, n0, warp * per, frag_row());
-  const BaRow x1 = ba_row(a, head, len, n0, warp * per, frag_row() + 8);
-  uint32_t qf[D / 16][4], df[D / 16][4];
-  load_rows<D>(qf, x0.row >= 0 ? a.out + x0.row * D : nullptr, x1.row >= 0 ? a.out + x1.row * D : nullptr);
-  load_rows<D>(df, x0.row >= 0 ? a.dout + x0.row * D : nullptr, x1.row >= 0 ? a.dout + x1.row * D : nullptr);
-  float d0 = 0.f, d1 = 0.f;
-#pragma unroll
-  for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float p = __uint_as_float(qf[ks][e] << 16) * __uint_as_float(df[ks][e] << 16) +
-                      __uint_as_float(qf[ks][e] & 0xFFFF0000u) * __uint_as_float(df[ks][e] & 0xFFFF0000u);
-      if (e & 1) d1 += p;
-      else d0 += p;
-    }
-  d0 = quad_sum(d0);
-  d1 = quad_sum(d1);
-  if ((lane_id() & 3) == 0) {
-    if (x0.row >= 0) a.delta[x0.row] = d0;
-    if (x1.row >= 0) a.delta[x1.row] = d1;
-  }
-  load_rows<D>(qf, x0.row >= 0 ? a.q + x0.row * D : nullptr, x1.row >= 0 ? a.q + x1.row * D : nullptr);
-  const float z0 = x0.row >= 0 ? a.lse_in[x0.row] * 1.4426950408889634f : 0.f;
-  const float z1 = x1.row >= 0 ? a.lse_in[x1.row] * 1.4426950408889634f : 0.f;
-  const __nv_bfloat16 *kh = a.k + static_cast<int64_t>(head) * a.Nk * D;
-  const __nv_bfloat16 *vh = a.v + static_cast<int64_t>(head) * a.Nk * D;
-  float acc[NT][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
-  const uint32_t base = smem_u32(smem);
-  auto key_of = [&](int u) { return static_cast<int>(list[u / sub]) * a.block + (u % sub) * kBaTile; };
-  auto fetch = [&](int u) {
-    if (u < total) {
-      const uint32_t buf = base + static_cast<uint32_t>(u & 1) * 2 * TILE;
-      load_tile<D, kBaThreads, kBaTile>(buf, kh, key_of(u), len, threadIdx.x);
-      load_tile<D, kBaThreads, kBaTile>(buf + TILE, vh, key_of(u), len, threadIdx.x);
-    }
-    cp_async_commit();
-  };
-  fetch(0);
-  for (int u = 0; u < total; ++u) {
-    fetch(u + 1);
-    cp_async_wait<1>();
-    __syncthreads();
-    const int blk = list[u / sub], key0 = key_of(u);
-    const bool on0 = x0.row >= 0 && ((bits[(blk >> 5) * tokens + x0.tok] >> (blk & 31)) & 1u) && key0 < x0.seen;
-    const bool on1 = x1.row >= 0 && ((bits[(blk >> 5) * tokens + x1.tok] >> (blk & 31)) & 1u) && key0 < x1.seen;
-    if (__any_sync(0xffffffffu, on0 || on1)) {
-      const uint32_t tile = base + static_cast<uint32_t>(u & 1) * 2 * TILE;
-      const uint32_t kt = lane_b<D>(tile), vt = kt + TILE, kx = lane_a<D>(tile);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float s[4][4], dp[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][e] = dp[t][e] = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-#pragma unroll
-          for (int t = 0; t < 4; t += 2) {
-            uint32_t b[4];
-            ldsm_x4(piece<D>(kt, 32 * h + 8 * t, ks), b);
-            mma_bf16(s[t], qf[ks], b[0], b[1]);
-            mma_bf16(s[t + 1], qf[ks], b[2], b[3]);
-            ldsm_x4(piece<D>(vt, 32 * h + 8 * t, ks), b);
-            mma_bf16(dp[t], df[ks], b[0], b[1]);
-            mma_bf16(dp[t + 1], df[ks], b[2], b[3]);
-          }
-        const int end0 = on0 ? x0.seen - key0 : 0, end1 = on1 ? x1.seen - key0 : 0;
-        uint32_t ds[2][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int c = 32 * h + 8 * t + frag_col();
-          float g[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool in = c + (e & 1) < (e < 2 ? end0 : end1);
-            const float pr = ex2_approx(s[t][e] * a.scale_log2 - (e < 2 ? z0 : z1));
-            g[e] = in ? pr * (dp[t][e] - (e < 2 ? d0 : d1)) : 0.f;
-          }
-          ds[t / 2][(t & 1) * 2] = pack_bf16(g[0], g[1]);
-          ds[t / 2][(t & 1) * 2 + 1] = pack_bf16(g[2], g[3]);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; t += 4) {
-          float c[4][4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c[j][e] = acc[t + j][e];
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              uint32_t b[4];
-              ldsm_x4_trans(piece<D>(kx, 32 * h + 16 * ks, (t + j) / 2), b);
-              mma_bf16(c[j], ds[ks], b[0], b[1]);
-              mma_bf16(c[j + 1], ds[ks], b[2], b[3]);
-            }
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t + j][e] = (e < 2 ? on0 : on1) ? c[j][e] : acc[t + j][e];
-        }
-      }
-    }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int c = 8 * t + frag_col();
-    if (x0.row >= 0)
-      *reinterpret_cast<uint32_t *>(a.dq + x0.row * D + c) = pack_bf16(acc[t][0] * a.scale, acc[t][1] * a.scale);
-    if (x1.row >= 0)
-      *reinterpret_cast<uint32_t *>(a.dq + x1.row * D + c) = pack_bf16(acc[t][2] * a.scale, acc[t][3] * a.scale);
-  }
-}
-
 // Who lists a block: bit sets over the queries (order of the atomics is of no
 // account).
 __global__ void __launch_bounds__(256) block_attn_reverse_kernel(const BlockAttnArgs a) {
@@ -623,190 +482,6 @@ __global__ void __launch_bounds__(1024) block_attn_items_kernel(const BlockAttnA
     __syncthreads();
   }
   if (threadIdx.x == 0) a.item_first[tiles] = static_cast<int>(carry >> 32);
-}
-
-// dK and dV of one key tile over up to item_tokens of the queries that list its
-// block: 4 warps x 16 keys, 64 gathered (query, head) rows at a time.
-//   S^T = K Q^T, P^T = exp(S^T - lse), dV += P^T dO, dP^T = V dO^T, dK += dS^T Q
-// A tile with one item is stored, others go to fp32 slots summed in order.
-constexpr int kBaRows = 64;
-template <int D>
-__host__ __device__ inline size_t block_attn_dkv_smem(int item_tokens) {
-  return static_cast<size_t>(4) * kBaRows * D * 2 + static_cast<size_t>(2) * kBaRows * 12 +
-         static_cast<size_t>(item_tokens) * 4 + 64;
-}
-
-template <int D>
-__global__ void __launch_bounds__(kBaThreads) block_attn_dkv_kernel(const BlockAttnArgs a) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int TILE = kBaRows * D * 2, NT = D / 8, COLS = D / 8;
-  const int sub = a.block / kBaTile;
-  const int tiles = a.BHk * a.nblk * sub;
-  const int nitems = a.item_first[tiles];
-  const int item = blockIdx.x;
-  if (item >= nitems) return;
-  const int tile = a.items[item];
-  const int first = a.item_first[tile];
-  const bool alone = a.item_first[tile + 1] - first == 1;
-  const int64_t blk = tile / sub;
-  const int head = static_cast<int>(blk / a.nblk);
-  const int key0 = static_cast<int>(blk % a.nblk) * a.block + (tile % sub) * kBaTile;
-  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
-  const int warp = warp_id(), lane = lane_id();
-  float *row_lse = reinterpret_cast<float *>(smem + 4 * TILE);      // [2][64]
-  float *row_delta = row_lse + 2 * kBaRows;
-  int *row_seen = reinterpret_cast<int *>(row_delta + 2 * kBaRows);
-  int *warp_sum = row_seen + 2 * kBaRows;      // [4]
-  int *toks = warp_sum + 4;
-
-  // this item's queries: places [skip, skip + item_tokens) of the block's bit set
-  const int skip = (item - first) * a.item_tokens;
-  const int WQ = (a.Nq + 31) / 32;
-  const uint32_t *rev = a.rev + blk * WQ;
-  int carry = 0;
-  for (int w0 = 0; w0 < WQ; w0 += kBaThreads) {
-    const int w = w0 + threadIdx.x;
-    uint32_t u = w < WQ ? rev[w] : 0u;
-    int x = __popc(u);
-    const int own = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) warp_sum[warp] = x;
-    __syncthreads();
-    int at = carry + x - own - skip;
-    for (int i = 0; i < 4; ++i) {
-      if (i < warp) at += warp_sum[i];
-      carry += warp_sum[i];
-    }
-    while (u) {
-      if (at >= 0 && at < a.item_tokens) toks[at] = w * 32 + __ffs(u) - 1;
-      u &= u - 1;
-      ++at;
-    }
-    __syncthreads();
-  }
-  const int ntok = min(max(carry - skip, 0), a.item_tokens);
-  const int rows = ntok * a.G;
-
-  const uint32_t base = smem_u32(smem);
-  const int64_t qbase = static_cast<int64_t>(head) * a.G * a.Nq;
-  auto fetch = [&](int r0, int st) {
-    if (r0 < rows) {
-      const uint32_t qt = base + static_cast<uint32_t>(st) * 2 * TILE, dt = qt + TILE;
-      for (int i = threadIdx.x; i < kBaRows * COLS; i += kBaThreads) {
-        const int r = i / COLS, c = i % COLS;
-        const bool in = r0 + r < rows;
-        const int n = in ? toks[(r0 + r) / a.G] : 0;
-        const int64_t src = (qbase + static_cast<int64_t>((r0 + r) % a.G) * a.Nq + n) * D + 8 * c;
-        cp_async16(qt + tile_at<D>(r, c), a.q + (in ? src : 0), in ? 16u : 0u);
-        cp_async16(dt + tile_at<D>(r, c), a.dout + (in ? src : 0), in ? 16u : 0u);
-      }
-      if (threadIdx.x < kBaRows) {
-        const int r = r0 + threadIdx.x;
-        const bool in = r < rows;
-        const int n = in ? toks[r / a.G] : 0;
-        const int64_t src = qbase + static_cast<int64_t>(r % a.G) * a.Nq + n;
-        row_lse[st * kBaRows + threadIdx.x] = in ? a.lse_in[src] * 1.4426950408889634f : 0.f;
-        row_delta[st * kBaRows + threadIdx.x] = in ? a.delta[src] : 0.f;
-        row_seen[st * kBaRows + threadIdx.x] = in ? query_seen(a, len, n) : 0;
-      }
-    }
-    cp_async_commit();
-  };
-
-  uint32_t kf[D / 16][4], vf[D / 16][4];
-  const int ka = key0 + 16 * warp + frag_row(), kb = ka + 8;
-  {
-    const int64_t hk = static_cast<int64_t>(head) * a.Nk;
-    load_rows<D>(kf, ka < len ? a.k + (hk + ka) * D : nullptr, kb < len ? a.k + (hk + kb) * D : nullptr);
-    load_rows<D>(vf, ka < len ? a.v + (hk + ka) * D : nullptr, kb < len ? a.v + (hk + kb) * D : nullptr);
-  }
-  float dk[NT][4], dv[NT][4];
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) dk[t][e] = dv[t][e] = 0.f;
-
-  fetch(0, 0);
-  for (int r0 = 0, st = 0; r0 < rows; r0 += kBaRows, st ^= 1) {
-    fetch(r0 + kBaRows, st ^ 1);
-    cp_async_wait<1>();
-    __syncthreads();
-    const uint32_t tile = base + static_cast<uint32_t>(st) * 2 * TILE;
-    const uint32_t qb = lane_b<D>(tile), qa = lane_a<D>(tile);      // dO's tile lies behind Q's
-#pragma unroll 1
-    for (int rs = 0; rs < kBaRows; rs += 16) {
-      if (r0 + rs >= rows) break;
-      float s[2][4], dp[2][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = dp[t][e] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        uint32_t b[4];
-        ldsm_x4(piece<D>(qb, rs, ks), b);
-        mma_bf16(s[0], kf[ks], b[0], b[1]);
-        mma_bf16(s[1], kf[ks], b[2], b[3]);
-        ldsm_x4(piece<D>(qb + TILE, rs, ks), b);
-        mma_bf16(dp[0], vf[ks], b[0], b[1]);
-        mma_bf16(dp[1], vf[ks], b[2], b[3]);
-      }
-      uint32_t pf[4], gf[4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float p[4], g[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = st * kBaRows + rs + 8 * t + frag_col() + (e & 1);
-          const bool in = (e < 2 ? ka : kb) < row_seen[r];
-          p[e] = in ? ex2_approx(s[t][e] * a.scale_log2 - row_lse[r]) : 0.f;
-          g[e] = in ? p[e] * (dp[t][e] - row_delta[r]) : 0.f;
-        }
-        pf[2 * t] = pack_bf16(p[0], p[1]);
-        pf[2 * t + 1] = pack_bf16(p[2], p[3]);
-        gf[2 * t] = pack_bf16(g[0], g[1]);
-        gf[2 * t + 1] = pack_bf16(g[2], g[3]);
-      }
-#pragma unroll
-      for (int t = 0; t < NT; t += 2) {
-        uint32_t b[4];
-        ldsm_x4_trans(piece<D>(qa + TILE, rs, t / 2), b);
-        mma_bf16(dv[t], pf, b[0], b[1]);
-        mma_bf16(dv[t + 1], pf, b[2], b[3]);
-        ldsm_x4_trans(piece<D>(qa, rs, t / 2), b);
-        mma_bf16(dk[t], gf, b[0], b[1]);
-        mma_bf16(dk[t + 1], gf, b[2], b[3]);
-      }
-    }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
-#pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int key = half ? kb : ka;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int c = 8 * t + frag_col();
-      const float k0 = dk[t][2 * half] * a.scale, k1 = dk[t][2 * half + 1] * a.scale;
-      const float v0 = dv[t][2 * half], v1 = dv[t][2 * half + 1];
-      if (alone) {
-        if (key < a.Nk) {
-          const int64_t at = (static_cast<int64_t>(head) * a.Nk + key) * D + c;
-          *reinterpret_cast<uint32_t *>(a.dk + at) = pack_bf16(k0, k1);
-          *reinterpret_cast<uint32_t *>(a.dv + at) = pack_bf16(v0, v1);
-        }
-      } else {
-        float *slot = a.part_kv + static_cast<int64_t>(a.slot_first[tile] + item - first) * 2 * kBaTile * D +
-                      (key - key0) * D + c;
-        *reinterpret_cast<float2 *>(slot) = make_float2(k0, k1);
-        *reinterpret_cast<float2 *>(slot + kBaTile * D) = make_float2(v0, v1);
-      }
-    }
-  }
 }
 
 // Sum of the items of a key tile with several: one CTA per tile.

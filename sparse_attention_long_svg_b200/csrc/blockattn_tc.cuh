@@ -43,10 +43,10 @@ __device__ __forceinline__ void tc_load_tile(uint32_t dst, const __nv_bfloat16 *
 
 // A 128-row operand tile (row r of the CTA = row(r) of a [rows, D] matrix, -1:
 // zeros) by all threads.
-template <int D, typename F>
+template <int D, int THREADS, typename F>
 __device__ __forceinline__ void tc_load_rows(uint32_t dst, const __nv_bfloat16 *src, F row) {
   constexpr int COLS = D / 8;
-  for (int i = threadIdx.x; i < kTcRows * COLS; i += kTcThreads) {
+  for (int i = threadIdx.x; i < kTcRows * COLS; i += THREADS) {
     const int r = i / COLS, c = i % COLS;
     const int64_t at = row(r);
     cp_async16(dst + tc_at<kTcRows>(r, c), src + (at >= 0 ? at * D + 8 * c : 0), at >= 0 ? 16u : 0u);
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   uint8_t *sKV = smem + Q_BYTES;                    // [stage][K, V]
   TcBars *B = reinterpret_cast<TcBars *>(sKV + 4 * KV);
   uint32_t *bits = reinterpret_cast<uint32_t *>(sKV + 4 * KV + 192);
-  const int tokens = kTcRows / a.G;
+  const int tokens = a.tile_tokens;
   const int W = (a.nblk + 31) / 32;
   uint32_t *uni = bits + tokens * W;
   uint16_t *list = reinterpret_cast<uint16_t *>(uni + W);
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
     mbar_init(&B->drain, 1);
     fence_mbar_init();
   }
-  tc_load_rows<D>(smem_u32(smem), a.q, row_of);
+  tc_load_rows<D, kTcThreads>(smem_u32(smem), a.q, row_of);
   cp_async_commit();
   TcUnion un;
   un.list = list;
@@ -428,6 +428,576 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   }
   __syncthreads();
   if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, COLS);
+  }
+}
+
+
+// ------------------------------------------------------------------ gradient
+// One row of dQ by one warp, from its own keys alone (see row_again).
+template <int D>
+__device__ __noinline__ void dq_row_again(const TcUnion &un, const __nv_bfloat16 *q, const __nv_bfloat16 *dout,
+                                          const __nv_bfloat16 *k, const __nv_bfloat16 *v, int tok, int seen, float sl2,
+                                          float lse2, float delta, float (&y)[D / 32]) {
+  constexpr int E = D / 32;
+  const int lane = lane_id();
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = 0.f;
+  for (int u = un.u0; u < un.u1; ++u) {
+    if (!un.listed(tok, u)) continue;
+    const int key0 = un.key(u), end = min(seen - key0, kBaTile);
+    for (int j0 = 0; j0 < end; j0 += 32) {
+      float ds = 0.f;
+      if (j0 + lane < end) {
+        const int64_t at = static_cast<int64_t>(key0 + j0 + lane) * D;
+        ds = ex2_approx(dot_rows(q, k + at, D) * sl2 - lse2) * (dot_rows(dout, v + at, D) - delta);
+      }
+      for (int j = 0; j < min(32, end - j0); ++j) {
+        const float g = __shfl_sync(0xffffffffu, ds, j);
+        const __nv_bfloat16 *kr = k + static_cast<int64_t>(key0 + j0 + j) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y[e] += g * __bfloat162float(kr[e]);
+      }
+    }
+  }
+}
+
+// dQ, and delta for the second kernel.  As the forward kernel, but scores need
+// no running maximum, so two groups of four warps take the steps in turn (a TMEM
+// lane belongs to a thread of each): S and dP of a step lie in the group's
+// buffers, dS replaces S there as the A operand of the product with K.
+constexpr int kTcDqThreads = 11 * 32, kTcDqStages = 3;
+
+struct TcDqBars {                      // at most 256 bytes
+  uint64_t k_full[kTcDqStages], k_empty[kTcDqStages], v_full[kTcDqStages], v_empty[kTcDqStages], s_full[2], ds_full[2],
+      done, drain;
+  uint32_t tmem;
+  int count;
+};
+
+template <int D>
+__host__ __device__ inline size_t tc_dq_smem(int tokens, int nblk) {
+  return 2ull * kTcRows * D * 2 + 2ull * kTcDqStages * kBaTile * D * 2 + 256 + kTcRows * 8 + mark_bytes(tokens, nblk);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const BlockAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int Q_BYTES = kTcRows * D * 2, KV = kBaTile * D * 2, NS = kTcDqStages, COLS = 512;
+  constexpr uint32_t IDESC_S = idesc_bf16_f32(kTcRows, kBaTile, false, false);
+  constexpr uint32_t IDESC_DQ = idesc_bf16_f32(kTcRows, D, false, true);
+  constexpr uint32_t TM_S = D, TM_DP = D + 2 * kBaTile;
+  uint8_t *sK = smem + 2 * Q_BYTES, *sV = sK + NS * KV;
+  TcDqBars *B = reinterpret_cast<TcDqBars *>(sV + NS * KV);
+  float *row_lse = reinterpret_cast<float *>(sV + NS * KV + 256), *row_delta = row_lse + kTcRows;
+  uint32_t *bits = reinterpret_cast<uint32_t *>(row_delta + kTcRows);
+  const int tokens = a.tile_tokens;
+  const int W = (a.nblk + 31) / 32;
+  uint32_t *uni = bits + tokens * W;
+  uint16_t *list = reinterpret_cast<uint16_t *>(uni + W);
+  const int ntiles = (a.Nq + tokens - 1) / tokens;
+  const int head = blockIdx.x / ntiles;
+  const int n0 = (ntiles - 1 - static_cast<int>(blockIdx.x % ntiles)) * tokens;
+  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
+  const int warp = warp_id(), lane = lane_id();
+  const uint64_t ns = a.wait_ns;
+  auto row_of = [&](int r) -> int64_t {
+    const int n = n0 + r / a.G;
+    return r < tokens * a.G && n < a.Nq ? (static_cast<int64_t>(head) * a.G + r % a.G) * a.Nq + n : -1;
+  };
+  if (warp == 8) {
+    tmem_alloc(&B->tmem, COLS);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&B->k_full[i], 32);
+      mbar_init(&B->k_empty[i], 1);
+      mbar_init(&B->v_full[i], 32);
+      mbar_init(&B->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->s_full[i], 1);
+      mbar_init(&B->ds_full[i], 128);
+    }
+    mbar_init(&B->done, 1);
+    mbar_init(&B->drain, 1);
+    fence_mbar_init();
+  }
+  tc_load_rows<D, kTcDqThreads>(smem_u32(smem), a.q, row_of);
+  tc_load_rows<D, kTcDqThreads>(smem_u32(smem) + Q_BYTES, a.dout, row_of);
+  cp_async_commit();
+  TcUnion un;
+  un.list = list;
+  un.bits = bits;
+  un.shift = a.block == kBaTile ? 0 : 1;
+  un.tokens = tokens;
+  un.u0 = 0;
+  tc_fence_before();
+  un.u1 = mark_blocks(a, head, len, n0, tokens, W, bits, uni, list, &B->count) << un.shift;
+  tc_fence_after();
+  cp_async_wait<0>();
+  fence_proxy_async_smem();
+  __syncthreads();
+  // delta = rowsum(dO O): D/8 lanes to a row
+  for (int i = threadIdx.x; i < kTcRows * (D / 8); i += kTcDqThreads) {
+    const int r = i / (D / 8), c = i % (D / 8);
+    const int64_t row = row_of(r);
+    float s = 0.f;
+    if (row >= 0) {
+      float x[8], y[8];
+      unpack8(*reinterpret_cast<const uint4 *>(smem + Q_BYTES + tc_at<kTcRows>(r, c)), x);
+      unpack8(__ldg(reinterpret_cast<const uint4 *>(a.out + row * D + 8 * c)), y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += x[e] * y[e];
+    }
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (c == 0) {
+      row_delta[r] = s;
+      row_lse[r] = row >= 0 ? a.lse_in[row] * 1.4426950408889634f : 0.f;
+      if (row >= 0) a.delta[row] = s;
+    }
+  }
+  __syncthreads();
+  const uint32_t tmem = B->tmem;
+  const int steps = un.u1;
+  const __nv_bfloat16 *kh = a.k + static_cast<int64_t>(head) * a.Nk * D;
+  const __nv_bfloat16 *vh = a.v + static_cast<int64_t>(head) * a.Nk * D;
+
+  if (warp >= 9) {
+    // ---------------------------------------------------------------- loads: K, V
+    const bool is_v = warp == 10;
+    uint64_t *full = is_v ? B->v_full : B->k_full, *empty = is_v ? B->v_empty : B->k_empty;
+    int st = 0, ph = 1;                             // the first round finds the stages empty
+    for (int t = 0; t < steps; ++t) {
+      if (t >= NS && !tc_warp_wait(&empty[st], ph, ns)) break;
+      tc_load_tile<D>(smem_u32(is_v ? sV : sK) + static_cast<uint32_t>(st) * KV, is_v ? vh : kh, un.key(t), len);
+      cp_async_arrive(&full[st]);
+      if (++st == NS) {
+        st = 0;
+        ph ^= 1;
+      }
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- matrix products
+    if (lane == 0) {
+      const SmemDesc qd = make_desc_sw128(smem_u32(smem), 16, 1024);
+      const SmemDesc od = make_desc_sw128(smem_u32(smem) + Q_BYTES, 16, 1024);
+      const SmemDesc kd = make_desc_sw128(smem_u32(sK), 16, 1024);
+      const SmemDesc vd = make_desc_sw128(smem_u32(sV), 16, 1024);
+      const SmemDesc kn = make_desc_sw128(smem_u32(sK), kBaTile * 128, 1024);
+      int st = 0, ph = 0;
+      auto issue_s = [&](int t) {                   // S and dP of step t, into the buffers of its group
+        if (!tc_wait(&B->k_full[st], ph, ns) || !tc_wait(&B->v_full[st], ph, ns)) return false;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t off = static_cast<uint32_t>(st * KV) >> 4, buf = (t & 1) * kBaTile;
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + buf, qd, SmemDesc{kd.lo + off, kd.hi},
+                                                                IDESC_S, 0u);
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + buf, od, SmemDesc{vd.lo + off, vd.hi},
+                                                                IDESC_S, 0u);
+        mma_commit(&B->s_full[t & 1]);
+        mma_commit(&B->v_empty[st]);
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1;
+        }
+        return true;
+      };
+      int done = 0;                                 // stage of step t
+      bool ok = steps == 0 || issue_s(0);
+      for (int t = 0; t < steps && ok; ++t) {
+        // the buffers of step t + 1 held dS(t - 1), whose product was issued before
+        if (t + 1 < steps && !issue_s(t + 1)) break;
+        if (!tc_wait(&B->ds_full[t & 1], (t >> 1) & 1, ns)) break;
+        tc_fence_after();
+        const uint32_t off = static_cast<uint32_t>(done * KV) >> 4;
+#pragma unroll
+        for (int k = 0; k < kBaTile / 16; ++k)
+          mma_bf16_ts(tmem, tmem + TM_S + (t & 1) * kBaTile + 8 * k,
+                      (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + ((k * 2048) >> 4)), IDESC_DQ,
+                      t > 0 || k > 0 ? 1u : 0u);
+        mma_commit(&B->k_empty[done]);
+        if (t == steps - 1) mma_commit(&B->done);
+        if (++done == NS) done = 0;
+      }
+      mma_commit(&B->drain);
+      mbar_wait(&B->drain, 0, 1000000000ull);
+    }
+  } else {
+    // ---------------------------------------------------------------- dS
+    const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+    const int64_t row = row_of(r);
+    const int tok = row >= 0 ? r / a.G : 0;
+    const int seen = row >= 0 ? query_seen(a, len, n0 + tok) : 0;
+    const float z = row_lse[r], delta = row_delta[r];
+    const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_at = mine + TM_S + grp * kBaTile, p_at = mine + TM_DP + grp * kBaTile;
+    bool ok = true;
+    for (int t = grp; t < steps; t += 2) {
+      const int key0 = un.key(t);
+      const int end = row >= 0 && un.listed(tok, t) ? seen - key0 : 0;
+      if (!tc_warp_wait(&B->s_full[grp], (t >> 1) & 1, ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool any = __any_sync(0xffffffffu, end > 0), part = __any_sync(0xffffffffu, end > 0 && end < kBaTile);
+      float g[32];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (any) {
+          float s[32], dp[32];
+          tmem_ld32_sync(s_at + 32 * h, s);
+          tmem_ld32_sync(p_at + 32 * h, dp);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            float d[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float p = ex2_approx(fmaf(s[c + e], a.scale_log2, -z));
+              d[e] = p * (dp[c + e] - delta);
+              if (part) d[e] = 32 * h + c + e < end ? d[e] : 0.f;
+            }
+            // dS as bf16 for the matrix product: 2^-8 relative to each
+            g[16 * h + (c >> 1)] = end > 0 ? __uint_as_float(pack_bf16x2(d[0], d[1])) : 0.f;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) g[16 * h + c] = 0.f;
+        }
+      }
+      tmem_st32(s_at, g);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&B->ds_full[grp]);
+    }
+    if (grp == 0) {
+      // ---- the accumulator: scaled, stored, rows that are not finite again
+      if (ok && steps > 0) ok = tc_warp_wait(&B->done, 0, ns);
+      tc_fence_after();
+      bool bad = false;
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        if (ok && steps > 0) {
+          tmem_ld32_sync(mine + c, o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          float y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            y[i] = o[e + i] * a.scale;
+            bad = bad || !(fabsf(y[i]) < INFINITY);
+          }
+          if (row >= 0) *reinterpret_cast<uint4 *>(a.dq + row * D + c + e) = pack8(y);
+        }
+      }
+      for (uint32_t again = __ballot_sync(0xffffffffu, ok && row >= 0 && bad); again; again &= again - 1) {
+        const int src = __ffs(again) - 1;
+        const int64_t rw = __shfl_sync(0xffffffffu, row, src);
+        float y[D / 32];
+        dq_row_again<D>(un, a.q + rw * D, a.dout + rw * D, kh, vh, __shfl_sync(0xffffffffu, tok, src),
+                        __shfl_sync(0xffffffffu, seen, src), a.scale_log2, __shfl_sync(0xffffffffu, z, src),
+                        __shfl_sync(0xffffffffu, delta, src), y);
+#pragma unroll
+        for (int e = 0; e < D / 32; e += 2)
+          *reinterpret_cast<uint32_t *>(a.dq + rw * D + lane * (D / 32) + e) =
+              pack_bf16(y[e] * a.scale, y[e + 1] * a.scale);
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, COLS);
+  }
+}
+
+// dK and dV of one key tile over one work item's queries (see
+// block_attn_count_kernel): 128 gathered (query, head) rows a step.
+//   S = Q K^T, dP = dO V^T (rows x keys, double buffered in TMEM)
+//   dV^T += dO^T P, dK^T += Q^T dS (channels x keys; P and dS through shared
+//   memory, rows of keys, the MN-major B operand)
+// D = 64 would leave half of the 128 accumulator lanes empty, so there one
+// product [dO | Q]^T [P | dS] makes both (its other two quarters are not read).
+// Warps 0-7: two groups, 32 keys each; warp 8: matrix products; warps 9-12: loads.
+constexpr int kTcDkvThreads = 13 * 32;
+
+struct TcDkvBars {                     // at most 128 bytes
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full, p_free, done, drain;
+  uint32_t tmem;
+  int warp_sum[4];
+};
+
+template <int D>
+__host__ __device__ inline size_t tc_dkv_smem(int item_tokens) {
+  return 2ull * kBaTile * D * 2 + 4ull * kTcRows * D * 2 + 2ull * kTcRows * 128 + 128 + static_cast<size_t>(item_tokens) * 4;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(const BlockAttnArgs a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  constexpr int KV = kBaTile * D * 2, QT = kTcRows * D * 2, PT = kTcRows * 128, COLS = 512;
+  constexpr uint32_t IDESC_S = idesc_bf16_f32(kTcRows, kBaTile, false, false);
+  constexpr uint32_t IDESC_G = idesc_bf16_f32(128, D == 128 ? kBaTile : 128, true, true);
+  constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DV = 256, TM_DK = 320;
+  uint8_t *sK = smem, *sV = sK + KV, *sQ = sV + KV;          // [stage][dO, Q]
+  uint8_t *sP = sQ + 4 * QT, *sG = sP + PT;
+  TcDkvBars *B = reinterpret_cast<TcDkvBars *>(sG + PT);
+  int *toks = reinterpret_cast<int *>(sG + PT + 128);
+  const int sub = a.block / kBaTile;
+  const int tiles = a.BHk * a.nblk * sub;
+  const int item = blockIdx.x;
+  if (item >= a.item_first[tiles]) return;
+  const int tile = a.items[item];
+  const int first = a.item_first[tile];
+  const bool alone = a.item_first[tile + 1] - first == 1;
+  const int64_t blk = tile / sub;
+  const int head = static_cast<int>(blk / a.nblk);
+  const int key0 = static_cast<int>(blk % a.nblk) * a.block + (tile % sub) * kBaTile;
+  const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
+  const int warp = warp_id(), lane = lane_id();
+  const uint64_t ns = a.wait_ns;
+  if (warp == 8) {
+    tmem_alloc(&B->tmem, COLS);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->q_full[i], 128);
+      mbar_init(&B->q_empty[i], 1);
+      mbar_init(&B->s_full[i], 1);
+    }
+    mbar_init(&B->p_full, 256);
+    mbar_init(&B->p_free, 1);
+    mbar_init(&B->done, 1);
+    mbar_init(&B->drain, 1);
+    fence_mbar_init();
+  }
+  if (warp >= 11) {
+    tc_load_tile<D>(smem_u32(warp == 11 ? sK : sV),
+                    (warp == 11 ? a.k : a.v) + static_cast<int64_t>(head) * a.Nk * D, key0, len);
+    cp_async_commit();
+  }
+  // this item's queries: places [skip, skip + item_tokens) of the block's bit set
+  const int skip = (item - first) * a.item_tokens;
+  const int WQ = (a.Nq + 31) / 32;
+  const uint32_t *rev = a.rev + blk * WQ;
+  int carry = 0;
+  for (int w0 = 0; w0 < WQ; w0 += 128) {
+    if (warp < 4) {
+      const int w = w0 + threadIdx.x;
+      uint32_t u = w < WQ ? rev[w] : 0u;
+      int x = __popc(u);
+      const int own = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) B->warp_sum[warp] = x;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      int at = carry + x - own - skip;
+      for (int i = 0; i < 4; ++i) {
+        if (i < warp) at += B->warp_sum[i];
+        carry += B->warp_sum[i];
+      }
+      for (; u; u &= u - 1, ++at)
+        if (at >= 0 && at < a.item_tokens) toks[at] = w * 32 + __ffs(u) - 1;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+    }
+  }
+  if (threadIdx.x == 0) B->warp_sum[0] = carry;
+  cp_async_wait<0>();
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+  const int rows = min(max(B->warp_sum[0] - skip, 0), a.item_tokens) * a.G;
+  const int steps = (rows + kTcRows - 1) / kTcRows;
+  const int64_t qbase = static_cast<int64_t>(head) * a.G * a.Nq;
+  // (query, head) row i of the item as a row of [BHk*G*Nq], and its query
+  auto source = [&](int i, int &n) {
+    n = toks[i / a.G];
+    return qbase + static_cast<int64_t>(i % a.G) * a.Nq + n;
+  };
+
+  if (warp >= 9) {
+    // ---------------------------------------------------------------- loads: 32 rows a warp
+    constexpr int COLS16 = D / 8, PER = 32 / COLS16;
+    const int base_row = (warp - 9) * 32, c = lane % COLS16;
+    for (int t = 0; t < steps; ++t) {
+      const int st = t & 1;
+      if (t >= 2 && !tc_warp_wait(&B->q_empty[st], ((t >> 1) - 1) & 1, ns)) break;
+      const int i = t * kTcRows + base_row + lane;
+      int n;
+      const int64_t at = i < rows ? source(i, n) : -1;
+      const uint32_t dst = smem_u32(sQ) + static_cast<uint32_t>(st) * 2 * QT;
+#pragma unroll 8
+      for (int j = 0; j < 32; j += PER) {
+        const int r = j + lane / COLS16;
+        const int64_t from = __shfl_sync(0xffffffffu, at, r);
+        const uint32_t to = dst + tc_at<kTcRows>(base_row + r, c);
+        const int64_t src = from >= 0 ? from * D + 8 * c : 0;
+        cp_async16(to, a.dout + src, from >= 0 ? 16u : 0u);
+        cp_async16(to + QT, a.q + src, from >= 0 ? 16u : 0u);
+      }
+      cp_async_arrive(&B->q_full[st]);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- matrix products
+    if (lane == 0) {
+      const SmemDesc od = make_desc_sw128(smem_u32(sQ), 16, 1024), qd = make_desc_sw128(smem_u32(sQ) + QT, 16, 1024);
+      const SmemDesc kd = make_desc_sw128(smem_u32(sK), 16, 1024), vd = make_desc_sw128(smem_u32(sV), 16, 1024);
+      // transposed operands: 64 channels (keys) of all rows, then the next 64
+      const SmemDesc ot = make_desc_sw128(smem_u32(sQ), kTcRows * 128, 1024);
+      const SmemDesc qt = make_desc_sw128(smem_u32(sQ) + QT, kTcRows * 128, 1024);
+      const SmemDesc pd = make_desc_sw128(smem_u32(sP), PT, 1024), gd = make_desc_sw128(smem_u32(sG), PT, 1024);
+      auto issue_s = [&](int t) {
+        const int st = t & 1;
+        if (!tc_wait(&B->q_full[st], (t >> 1) & 1, ns)) return false;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, SmemDesc{qd.lo + off, qd.hi},
+                                                                kd, IDESC_S, 0u);
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + st * kBaTile,
+                                                                SmemDesc{od.lo + off, od.hi}, vd, IDESC_S, 0u);
+        mma_commit(&B->s_full[st]);
+        return true;
+      };
+      bool ok = steps == 0 || issue_s(0);
+      for (int t = 0; t < steps && ok; ++t) {
+        const int st = t & 1;
+        // step t + 1's buffers were read before P(t - 1) was announced
+        if (t + 1 < steps && !issue_s(t + 1)) break;
+        if (!tc_wait(&B->p_full, t & 1, ns)) break;
+        tc_fence_after();
+        const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
+        const uint32_t more = t > 0 ? 1u : 0u;
+        // K steps of 16 rows = 2048 bytes in both operands
+        mma_chain<kTcRows / 16, 4 * 2048, 2048, 4 * 2048, 2048>(tmem + TM_DV, SmemDesc{ot.lo + off, ot.hi}, pd, IDESC_G,
+                                                                more);
+        if (D == 128)
+          mma_chain<kTcRows / 16, 4 * 2048, 2048, 4 * 2048, 2048>(tmem + TM_DK, SmemDesc{qt.lo + off, qt.hi}, gd,
+                                                                  IDESC_G, more);
+        mma_commit(&B->q_empty[st]);
+        mma_commit(&B->p_free);
+        if (t == steps - 1) mma_commit(&B->done);
+      }
+      mma_commit(&B->drain);
+      mbar_wait(&B->drain, 0, 1000000000ull);
+    }
+  } else {
+    // ---------------------------------------------------------------- P and dS
+    const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    float z_next = 0.f, d_next = 0.f;
+    int seen_next = 0;
+    auto row_values = [&](int t) {                  // of the next step, while this one is computed
+      const int i = t * kTcRows + r;
+      seen_next = 0;
+      z_next = d_next = 0.f;
+      if (t < steps && i < rows) {
+        int n;
+        const int64_t at = source(i, n);
+        z_next = __ldg(a.lse_in + at);
+        d_next = a.delta[at];
+        seen_next = query_seen(a, len, n);
+      }
+    };
+    row_values(0);
+    bool ok = true;
+    for (int t = 0; t < steps; ++t) {
+      const int st = t & 1;
+      const float z = z_next * 1.4426950408889634f, delta = d_next;
+      const int end = seen_next - key0 - 32 * grp;            // keys of this thread's 32 that the row sees
+      row_values(t + 1);
+      if (!tc_warp_wait(&B->s_full[st], (t >> 1) & 1, ns)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float s[32], dp[32];
+      tmem_ld32_sync(mine + TM_S + st * kBaTile + 32 * grp, s);
+      tmem_ld32_sync(mine + TM_DP + st * kBaTile + 32 * grp, dp);
+      uint32_t p[16], g[16];
+      const bool part = __any_sync(0xffffffffu, end < 32);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float w[2], d[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          w[e] = ex2_approx(fmaf(s[c + e], a.scale_log2, -z));
+          d[e] = w[e] * (dp[c + e] - delta);
+          if (part) {
+            w[e] = c + e < end ? w[e] : 0.f;
+            d[e] = c + e < end ? d[e] : 0.f;
+          }
+        }
+        // bf16 for the matrix products: 2^-8 relative to each
+        p[c >> 1] = pack_bf16x2(w[0], w[1]);
+        g[c >> 1] = pack_bf16x2(d[0], d[1]);
+      }
+      if (t > 0 && !tc_warp_wait(&B->p_free, (t - 1) & 1, ns)) {
+        ok = false;
+        break;
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t at = tc_at<kTcRows>(r, 4 * grp + c);
+        *reinterpret_cast<uint4 *>(sP + at) = make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+        *reinterpret_cast<uint4 *>(sG + at) = make_uint4(g[4 * c], g[4 * c + 1], g[4 * c + 2], g[4 * c + 3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&B->p_full);
+    }
+    // ---- dV (group 0, or lanes 0-63) and dK: thread = channel, columns = keys
+    if (ok && steps > 0) ok = tc_warp_wait(&B->done, 0, ns);
+    tc_fence_after();
+    const bool is_k = D == 128 ? grp == 1 : r >= 64;
+    const int ch = D == 128 ? r : r & 63;
+    const float scale = is_k ? a.scale : 1.f;
+    if (D == 128 || grp == 0) {
+      const uint32_t from = mine + (is_k ? TM_DK : TM_DV);
+      __nv_bfloat16 *out = (is_k ? a.dk : a.dv) + (static_cast<int64_t>(head) * a.Nk + key0) * D + ch;
+      float *slot = a.part_kv + (static_cast<int64_t>(a.slot_first[tile] + item - first) * 2 + !is_k) * kBaTile * D + ch;
+#pragma unroll 1
+      for (int c = 0; c < kBaTile; c += 32) {
+        float v[32];
+        if (ok && steps > 0) {
+          tmem_ld32_sync(from + c, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          if (alone) {
+            if (key0 + c + e < a.Nk) out[static_cast<int64_t>(c + e) * D] = __float2bfloat16_rn(v[e] * scale);
+          } else {
+            slot[(c + e) * D] = v[e] * scale;
+          }
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, COLS);
   }

@@ -1024,6 +1024,16 @@ SelectArgs carve_select(void *ws, int BHk, int Nq, int nblk, int D, size_t *byte
   return a;
 }
 
+constexpr size_t kMaxSmem = 227 * 1024;
+// Tokens of a 128-row tile: as many as fit with their bit sets (fewer only for
+// one or two heads to a key head and thousands of blocks).
+template <typename F>
+int tile_tokens(int G, F smem) {
+  int t = kTcRows / G;
+  while (smem(t) > kMaxSmem) t = (t + 1) / 2;
+  return t;
+}
+
 struct BlockAttnPlan {
   bool few;
   int tokens, tiles, splits;
@@ -1034,7 +1044,7 @@ BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int 
   BlockAttnPlan p;
   const int per = 16 / (BHq / BHk);
   p.few = Nq <= per;
-  p.tokens = p.few ? per : kTcRows / (BHq / BHk);
+  p.tokens = p.few ? per : tile_tokens(BHq / BHk, [&](int t) { return tc_smem<128>(1, t, nblk); });
   p.tiles = (Nq + p.tokens - 1) / p.tokens;
   const int64_t ctas = static_cast<int64_t>(BHk) * p.tiles;
   const int64_t listed = static_cast<int64_t>(Nq < p.tokens ? Nq : p.tokens) * topk;
@@ -1048,7 +1058,7 @@ BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int 
 }
 
 // Gradient: rows of one work item (a key tile's queries beyond it go to more).
-constexpr int kBaItemRows = 2048;
+constexpr int kBaItemRows = 4096;
 struct BlockGradWs {
   float *delta, *part_kv;
   uint32_t *rev;
@@ -1231,6 +1241,7 @@ svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, 
   a.o = static_cast<__nv_bfloat16 *>(o);
   a.lse = lse;
   a.splits = p.splits;
+  a.tile_tokens = p.tokens;
   if (p.splits > 1) {
     Carve c{static_cast<uint8_t *>(ws)};
     a.part_o = c.take<float>(static_cast<size_t>(BHq) * Nq * p.splits * D);
@@ -1295,7 +1306,7 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
   const int sub = block / kBaTile;
   const int64_t tiles = static_cast<int64_t>(BHk) * nblk * sub;
   const int64_t listed = static_cast<int64_t>(BHk) * Nq * topk;
-  const int tokens = 4 * (16 / (BHq / BHk));
+  const int tokens = tile_tokens(BHq / BHk, [&](int t) { return D == 128 ? tc_dq_smem<128>(t, nblk) : tc_dq_smem<64>(t, nblk); });
   const int64_t ctas = static_cast<int64_t>(BHk) * ((Nq + tokens - 1) / tokens);
   if (tiles >= (1ll << 31) - 1 || w.max_items >= (1ll << 31) - 1 || (listed + 255) / 256 >= (1ll << 31) ||
       ctas >= (1ll << 31))
@@ -1315,6 +1326,7 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
   a.items = w.items;
   a.part_kv = w.part_kv;
   a.item_tokens = w.item_tokens;
+  a.tile_tokens = tokens;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = cuda_status(cudaMemsetAsync(w.rev, 0, w.rev_bytes, s), "cudaMemsetAsync(block lists)");
   if (st != SVG_OK) return st;
@@ -1325,16 +1337,16 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
   if (st != SVG_OK) return st;
   auto go = [&](auto dq_kernel, size_t dq_smem, auto dkv_kernel, size_t dkv_smem, auto join) {
     if (!set_smem(dq_kernel, dq_smem) || !set_smem(dkv_kernel, dkv_smem)) return SVG_ERR_CUDA;
-    dq_kernel<<<static_cast<unsigned>(ctas), kBaThreads, dq_smem, s>>>(a);
-    dkv_kernel<<<static_cast<unsigned>(w.max_items), kBaThreads, dkv_smem, s>>>(a);
+    dq_kernel<<<static_cast<unsigned>(ctas), kTcDqThreads, dq_smem, s>>>(a);
+    dkv_kernel<<<static_cast<unsigned>(w.max_items), kTcDkvThreads, dkv_smem, s>>>(a);
     join<<<static_cast<unsigned>(tiles), 256, 0, s>>>(a);
     return launch_status("block_attn gradient kernels");
   };
   if (D == 128)
-    return go(block_attn_dq_kernel<128>, block_attn_smem<128>(4 * kBaTile, tokens, nblk), block_attn_dkv_kernel<128>,
-              block_attn_dkv_smem<128>(w.item_tokens), block_attn_dkv_join_kernel<128>);
-  return go(block_attn_dq_kernel<64>, block_attn_smem<64>(4 * kBaTile, tokens, nblk), block_attn_dkv_kernel<64>,
-            block_attn_dkv_smem<64>(w.item_tokens), block_attn_dkv_join_kernel<64>);
+    return go(block_attn_dq_tc_kernel<128>, tc_dq_smem<128>(tokens, nblk), block_attn_dkv_tc_kernel<128>,
+              tc_dkv_smem<128>(w.item_tokens), block_attn_dkv_join_kernel<128>);
+  return go(block_attn_dq_tc_kernel<64>, tc_dq_smem<64>(tokens, nblk), block_attn_dkv_tc_kernel<64>,
+            tc_dkv_smem<64>(w.item_tokens), block_attn_dkv_join_kernel<64>);
 }
 
 }  // extern "C"
