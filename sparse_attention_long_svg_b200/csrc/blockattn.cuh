@@ -63,6 +63,9 @@ __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int
   for (int i = tid; i < tokens * W; i += threads) bits[i] = 0;
   const int32_t *sel = a.sel + (static_cast<int64_t>(head) * a.Nq + n0) * a.topk;
   const int ids = min(tokens, a.Nq - n0) * a.topk;
+  // i / topk for i < 2^18 (tokens <= 128, topk <= 1024): the rounding of the
+  // reciprocal adds less than 2^-14
+  const uint32_t per = 0xFFFFFFFFu / a.topk + 1;
   __syncthreads();
   for (int i0 = tid; i0 < ids; i0 += U * threads) {
     int j[U];
@@ -72,7 +75,7 @@ __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int
     for (int u = 0; u < U; ++u) {
       const int i = i0 + u * threads;
       if (i >= ids) break;
-      const int tok = i / a.topk;
+      const int tok = a.topk == 1 ? i : static_cast<int>(__umulhi(i, per));
       if (j[u] >= 0 && j[u] < a.nblk && static_cast<int64_t>(j[u]) * a.block < query_seen(a, len, n0 + tok))
         atomicOr(&bits[(j[u] >> 5) * tokens + tok], 1u << (j[u] & 31));
     }
@@ -98,7 +101,11 @@ __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int
         if (lane >= o) pre += x;
       }
       const int all = __shfl_sync(0xffffffffu, pre, 31);
-      for (int p = at + pre - own; u; u &= u - 1) list[p++] = static_cast<uint16_t>(w * 32 + __ffs(u) - 1);
+      for (int i = 0; i < min(32, W - w0); ++i) {   // word by word, a lane to a bit
+        const uint32_t x = __shfl_sync(0xffffffffu, u, i);
+        const int p = at + __shfl_sync(0xffffffffu, pre - own, i);
+        if ((x >> lane) & 1u) list[p + __popc(x & ((1u << lane) - 1))] = static_cast<uint16_t>((w0 + i) * 32 + lane);
+      }
       at += all;
     }
     if (lane == 0) *count = at;

@@ -41,15 +41,49 @@ __device__ __forceinline__ void tc_load_tile(uint32_t dst, const __nv_bfloat16 *
   }
 }
 
+// Row r < 128 of a tile: head r % G of token n0 + r / G, as a row of
+// [BHk*G, Nq] (-1: none).  The reciprocal of G is exact enough for r < 128.
+struct TcRowMap {
+  uint32_t per;
+  int G, n0, rows, Nq;
+  int64_t base;
+  __device__ __forceinline__ TcRowMap(const BlockAttnArgs &a, int head, int n0_, int tokens)
+      : per(65535u / a.G + 1), G(a.G), n0(n0_), rows(min(tokens, a.Nq - n0_) * a.G), Nq(a.Nq),
+        base(static_cast<int64_t>(head) * a.G * a.Nq) {}
+  __device__ __forceinline__ int token(int r) const { return static_cast<int>((r * per) >> 16); }
+  __device__ __forceinline__ int64_t operator()(int r) const {
+    const int t = token(r);
+    return r < rows ? base + static_cast<int64_t>(r - t * G) * Nq + n0 + t : -1;
+  }
+};
+
 // A 128-row operand tile (row r of the CTA = row(r) of a [rows, D] matrix, -1:
 // zeros) by all threads.
 template <int D, int THREADS, typename F>
 __device__ __forceinline__ void tc_load_rows(uint32_t dst, const __nv_bfloat16 *src, F row) {
   constexpr int COLS = D / 8;
-  for (int i = threadIdx.x; i < kTcRows * COLS; i += THREADS) {
-    const int r = i / COLS, c = i % COLS;
+#pragma unroll
+  for (int i0 = 0; i0 < kTcRows * COLS; i0 += THREADS) {
+    const int i = i0 + threadIdx.x, r = i / COLS, c = i % COLS;
+    if (i >= kTcRows * COLS) break;
     const int64_t at = row(r);
     cp_async16(dst + tc_at<kTcRows>(r, c), src + (at >= 0 ? at * D + 8 * c : 0), at >= 0 ? 16u : 0u);
+  }
+}
+
+// Which of two chains the issuing thread can go on with: 1 when `a` has
+// completed (and is wanted), else 2 when `b` has, 0 after `ns`.  A chain whose
+// operands are late must not hold up the other, which frees their buffers.
+__device__ __forceinline__ int tc_either(uint64_t *a, uint32_t pa, bool want_a, uint64_t *b, uint32_t pb, bool want_b,
+                                         uint64_t ns) {
+  const long long t0 = clock64(), limit = static_cast<long long>(ns) * 2;
+  while (true) {
+    if (want_a && mbar_test(a, pa)) return 1;
+    if (want_b && mbar_test(b, pb)) return 2;
+    if (clock64() - t0 > limit) {
+      record_error(SVG_ERR_TIMEOUT, SVG_SITE_BLOCK_ATTN);
+      return 0;
+    }
   }
 }
 
@@ -184,12 +218,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const int warp = warp_id(), lane = lane_id();
   const uint64_t ns = a.wait_ns;
-
-  // row r: head r % G of token n0 + r / G
-  auto row_of = [&](int r) -> int64_t {
-    const int n = n0 + r / a.G;
-    return r < tokens * a.G && n < a.Nq ? (static_cast<int64_t>(head) * a.G + r % a.G) * a.Nq + n : -1;
-  };
+  const TcRowMap row_of(a, head, n0, tokens);
   if (warp == 4) {
     tmem_alloc(&B->tmem, COLS);
     tmem_relinquish();
@@ -246,24 +275,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
       const SmemDesc qd = make_desc_sw128(smem_u32(smem), 16, 1024);
       const SmemDesc kd = make_desc_sw128(smem_u32(sKV), 16, 1024);
       const SmemDesc vd = make_desc_sw128(smem_u32(sKV) + KV, kBaTile * 128, 1024);
-      auto issue_s = [&](int t) {
-        const int st = t & 1;
-        if (!tc_wait(&B->k_full[st], (t >> 1) & 1, ns)) return false;
-        fence_proxy_async_smem();                   // cp.async writes -> tensor-core reads
-        tc_fence_after();
-        const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, qd,
-                                                                SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
-        mma_commit(&B->s_full[st]);
-        mma_commit(&B->k_empty[st]);
-        return true;
-      };
-      bool ok = steps == 0 || issue_s(0);
-      for (int t = 0; t < steps && ok; ++t) {
-        const int st = t & 1;
-        // its score buffer held P(t-1), whose product was issued before
-        if (t + 1 < steps && !issue_s(t + 1)) break;
-        if (!tc_wait(&B->v_full[st], (t >> 1) & 1, ns) || !tc_wait(&B->p_full[st], (t >> 1) & 1, ns)) break;
+      for (int ns_done = 0, t = 0; t < steps;) {      // score products issued, value products issued
+        const int ss = ns_done & 1, st = t & 1;
+        // S(t + 1) goes before P(t) V; its buffer held P(t - 1), whose product was issued before
+        const int next = tc_either(&B->k_full[ss], (ns_done >> 1) & 1, ns_done < steps && ns_done <= t + 1,
+                                   &B->p_full[st], (t >> 1) & 1, t < ns_done, ns);
+        if (next == 0) break;
+        if (next == 1) {
+          fence_proxy_async_smem();                 // cp.async writes -> tensor-core reads
+          tc_fence_after();
+          const uint32_t off = static_cast<uint32_t>(ss * 2 * KV) >> 4;
+          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + ss * kBaTile, qd,
+                                                                  SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
+          mma_commit(&B->s_full[ss]);
+          mma_commit(&B->k_empty[ss]);
+          ++ns_done;
+          continue;
+        }
+        if (!tc_wait(&B->v_full[st], (t >> 1) & 1, ns)) break;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
@@ -274,6 +303,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
                       t > 0 || k > 0 ? 1u : 0u);
         mma_commit(&B->v_empty[st]);
         mma_commit(&B->done);
+        ++t;
       }
       mma_commit(&B->drain);                        // all retired before TMEM is released
       mbar_wait(&B->drain, 0, 1000000000ull);
@@ -282,7 +312,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
     // ---------------------------------------------------------------- softmax
     const int r = warp * 32 + lane;
     const int64_t row = row_of(r);
-    const int tok = row >= 0 ? r / a.G : 0;
+    const int tok = row >= 0 ? row_of.token(r) : 0;
     const int seen = row >= 0 ? query_seen(a, len, n0 + tok) : 0;
     const uint32_t mine = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float m = -INFINITY, l = 0.f;
@@ -502,10 +532,7 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
   const int len = seq_len(a.kv_len, head / a.heads_per_seq, a.Nk);
   const int warp = warp_id(), lane = lane_id();
   const uint64_t ns = a.wait_ns;
-  auto row_of = [&](int r) -> int64_t {
-    const int n = n0 + r / a.G;
-    return r < tokens * a.G && n < a.Nq ? (static_cast<int64_t>(head) * a.G + r % a.G) * a.Nq + n : -1;
-  };
+  const TcRowMap row_of(a, head, n0, tokens);
   if (warp == 8) {
     tmem_alloc(&B->tmem, COLS);
     tmem_relinquish();
@@ -528,6 +555,15 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
   tc_load_rows<D, kTcDqThreads>(smem_u32(smem), a.q, row_of);
   tc_load_rows<D, kTcDqThreads>(smem_u32(smem) + Q_BYTES, a.dout, row_of);
   cp_async_commit();
+  // O for delta: D/8 lanes to a row
+  constexpr int OL = (kTcRows * (D / 8) + kTcDqThreads - 1) / kTcDqThreads;
+  uint4 o_row[OL];
+#pragma unroll
+  for (int k = 0; k < OL; ++k) {
+    const int i = k * kTcDqThreads + threadIdx.x;
+    const int64_t row = i < kTcRows * (D / 8) ? row_of(i / (D / 8)) : -1;
+    o_row[k] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.out + row * D + 8 * (i % (D / 8)))) : make_uint4(0, 0, 0, 0);
+  }
   TcUnion un;
   un.list = list;
   un.bits = bits;
@@ -540,25 +576,27 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
   cp_async_wait<0>();
   fence_proxy_async_smem();
   __syncthreads();
-  // delta = rowsum(dO O): D/8 lanes to a row
-  for (int i = threadIdx.x; i < kTcRows * (D / 8); i += kTcDqThreads) {
-    const int r = i / (D / 8), c = i % (D / 8);
-    const int64_t row = row_of(r);
-    float s = 0.f;
-    if (row >= 0) {
-      float x[8], y[8];
-      unpack8(*reinterpret_cast<const uint4 *>(smem + Q_BYTES + tc_at<kTcRows>(r, c)), x);
-      unpack8(__ldg(reinterpret_cast<const uint4 *>(a.out + row * D + 8 * c)), y);
+  // delta = rowsum(dO O)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[e] * y[e];
-    }
+  for (int k = 0; k < OL; ++k) {
+    const int i = k * kTcDqThreads + threadIdx.x, r = i / (D / 8), c = i % (D / 8);
+    if (i >= kTcRows * (D / 8)) break;              // by whole warps
+    float x[8], y[8], s = 0.f;
+    unpack8(*reinterpret_cast<const uint4 *>(smem + Q_BYTES + tc_at<kTcRows>(r, c)), x);
+    unpack8(o_row[k], y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[e] * y[e];
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (c == 0) {
+      const int64_t row = row_of(r);
       row_delta[r] = s;
-      row_lse[r] = row >= 0 ? a.lse_in[row] * 1.4426950408889634f : 0.f;
       if (row >= 0) a.delta[row] = s;
     }
+  }
+  if (threadIdx.x < kTcRows) {
+    const int64_t row = row_of(threadIdx.x);
+    row_lse[threadIdx.x] = row >= 0 ? a.lse_in[row] * 1.4426950408889634f : 0.f;
   }
   __syncthreads();
   const uint32_t tmem = B->tmem;
@@ -590,30 +628,30 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
       const SmemDesc kd = make_desc_sw128(smem_u32(sK), 16, 1024);
       const SmemDesc vd = make_desc_sw128(smem_u32(sV), 16, 1024);
       const SmemDesc kn = make_desc_sw128(smem_u32(sK), kBaTile * 128, 1024);
-      int st = 0, ph = 0;
-      auto issue_s = [&](int t) {                   // S and dP of step t, into the buffers of its group
-        if (!tc_wait(&B->k_full[st], ph, ns) || !tc_wait(&B->v_full[st], ph, ns)) return false;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t off = static_cast<uint32_t>(st * KV) >> 4, buf = (t & 1) * kBaTile;
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + buf, qd, SmemDesc{kd.lo + off, kd.hi},
-                                                                IDESC_S, 0u);
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + buf, od, SmemDesc{vd.lo + off, vd.hi},
-                                                                IDESC_S, 0u);
-        mma_commit(&B->s_full[t & 1]);
-        mma_commit(&B->v_empty[st]);
-        if (++st == NS) {
-          st = 0;
-          ph ^= 1;
+      int st = 0, ph = 0, done = 0;                 // stage of the next scores, of the next dQ product
+      for (int n_s = 0, t = 0; t < steps;) {
+        // S and dP of step t + 1 go before dQ(t); their buffers held dS(t - 1), whose product was issued before
+        const int next = tc_either(&B->k_full[st], ph, n_s < steps && n_s <= t + 1, &B->ds_full[t & 1], (t >> 1) & 1,
+                                   t < n_s, ns);
+        if (next == 0) break;
+        if (next == 1) {
+          if (!tc_wait(&B->v_full[st], ph, ns)) break;
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t off = static_cast<uint32_t>(st * KV) >> 4, buf = (n_s & 1) * kBaTile;
+          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + buf, qd, SmemDesc{kd.lo + off, kd.hi},
+                                                                  IDESC_S, 0u);
+          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + buf, od, SmemDesc{vd.lo + off, vd.hi},
+                                                                  IDESC_S, 0u);
+          mma_commit(&B->s_full[n_s & 1]);
+          mma_commit(&B->v_empty[st]);
+          ++n_s;
+          if (++st == NS) {
+            st = 0;
+            ph ^= 1;
+          }
+          continue;
         }
-        return true;
-      };
-      int done = 0;                                 // stage of step t
-      bool ok = steps == 0 || issue_s(0);
-      for (int t = 0; t < steps && ok; ++t) {
-        // the buffers of step t + 1 held dS(t - 1), whose product was issued before
-        if (t + 1 < steps && !issue_s(t + 1)) break;
-        if (!tc_wait(&B->ds_full[t & 1], (t >> 1) & 1, ns)) break;
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(done * KV) >> 4;
 #pragma unroll
@@ -622,8 +660,8 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
                       (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + ((k * 2048) >> 4)), IDESC_DQ,
                       t > 0 || k > 0 ? 1u : 0u);
         mma_commit(&B->k_empty[done]);
-        if (t == steps - 1) mma_commit(&B->done);
         if (++done == NS) done = 0;
+        if (++t == steps) mma_commit(&B->done);
       }
       mma_commit(&B->drain);
       mbar_wait(&B->drain, 0, 1000000000ull);
@@ -632,7 +670,7 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
     // ---------------------------------------------------------------- dS
     const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
     const int64_t row = row_of(r);
-    const int tok = row >= 0 ? r / a.G : 0;
+    const int tok = row >= 0 ? row_of.token(r) : 0;
     const int seen = row >= 0 ? query_seen(a, len, n0 + tok) : 0;
     const float z = row_lse[r], delta = row_delta[r];
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -732,15 +770,15 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
 // Warps 0-7: two groups, 32 keys each; warp 8: matrix products; warps 9-12: loads.
 constexpr int kTcDkvThreads = 13 * 32;
 
-struct TcDkvBars {                     // at most 128 bytes
+struct TcDkvBars {                     // at most 256 bytes
   uint64_t q_full[2], q_empty[2], s_full[2], p_full, p_free, done, drain;
   uint32_t tmem;
-  int warp_sum[4];
+  int warp_sum[kTcDkvThreads / 32];
 };
 
 template <int D>
 __host__ __device__ inline size_t tc_dkv_smem(int item_tokens) {
-  return 2ull * kBaTile * D * 2 + 4ull * kTcRows * D * 2 + 2ull * kTcRows * 128 + 128 + static_cast<size_t>(item_tokens) * 4;
+  return 2ull * kBaTile * D * 2 + 4ull * kTcRows * D * 2 + 2ull * kTcRows * 128 + 256 + static_cast<size_t>(item_tokens) * 4;
 }
 
 template <int D>
@@ -753,7 +791,7 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
   uint8_t *sK = smem, *sV = sK + KV, *sQ = sV + KV;          // [stage][dO, Q]
   uint8_t *sP = sQ + 4 * QT, *sG = sP + PT;
   TcDkvBars *B = reinterpret_cast<TcDkvBars *>(sG + PT);
-  int *toks = reinterpret_cast<int *>(sG + PT + 128);
+  int *toks = reinterpret_cast<int *>(sG + PT + 256);
   const int sub = a.block / kBaTile;
   const int tiles = a.BHk * a.nblk * sub;
   const int item = blockIdx.x;
@@ -788,48 +826,47 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
                     (warp == 11 ? a.k : a.v) + static_cast<int64_t>(head) * a.Nk * D, key0, len);
     cp_async_commit();
   }
-  // this item's queries: places [skip, skip + item_tokens) of the block's bit set
+  // this item's queries: places [skip, skip + item_tokens) of the block's bit
+  // set; each warp takes a run of its words, counts, then writes
+  constexpr int WARPS = kTcDkvThreads / 32;
   const int skip = (item - first) * a.item_tokens;
   const int WQ = (a.Nq + 31) / 32;
   const uint32_t *rev = a.rev + blk * WQ;
-  int carry = 0;
-  for (int w0 = 0; w0 < WQ; w0 += 128) {
-    if (warp < 4) {
-      const int w = w0 + threadIdx.x;
-      uint32_t u = w < WQ ? rev[w] : 0u;
-      int x = __popc(u);
-      const int own = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) B->warp_sum[warp] = x;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-      int at = carry + x - own - skip;
-      for (int i = 0; i < 4; ++i) {
-        if (i < warp) at += B->warp_sum[i];
-        carry += B->warp_sum[i];
-      }
-      for (; u; u &= u - 1, ++at)
-        if (at >= 0 && at < a.item_tokens) toks[at] = w * 32 + __ffs(u) - 1;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+  const int run = ((WQ + WARPS - 1) / WARPS + 31) / 32 * 32, w_end = min(WQ, (warp + 1) * run);
+  int mine_count = 0;
+  for (int w = warp * run + lane; w < w_end; w += 32) mine_count += __popc(__ldg(rev + w));
+  mine_count = __reduce_add_sync(0xffffffffu, mine_count);
+  if (lane == 0) B->warp_sum[warp] = mine_count;
+  __syncthreads();
+  int at = -skip, listed = 0;
+  for (int i = 0; i < WARPS; ++i) {
+    if (i < warp) at += B->warp_sum[i];
+    listed += B->warp_sum[i];
+  }
+  for (int w0 = warp * run; w0 < w_end && at < a.item_tokens; w0 += 32) {
+    const uint32_t u = w0 + lane < w_end ? __ldg(rev + w0 + lane) : 0u;
+    for (int i = 0; i < 32; ++i) {                  // a lane to a bit
+      const uint32_t x = __shfl_sync(0xffffffffu, u, i);
+      const int p = at + __popc(x & ((1u << lane) - 1));
+      if (((x >> lane) & 1u) && p >= 0 && p < a.item_tokens) toks[p] = (w0 + i) * 32 + lane;
+      at += __popc(x);
     }
   }
-  if (threadIdx.x == 0) B->warp_sum[0] = carry;
   cp_async_wait<0>();
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B->tmem;
-  const int rows = min(max(B->warp_sum[0] - skip, 0), a.item_tokens) * a.G;
+  const int rows = min(max(listed - skip, 0), a.item_tokens) * a.G;
   const int steps = (rows + kTcRows - 1) / kTcRows;
   const int64_t qbase = static_cast<int64_t>(head) * a.G * a.Nq;
   // (query, head) row i of the item as a row of [BHk*G*Nq], and its query
+  const uint32_t per = 0xFFFFFFFFu / a.G + 1;       // i / G for i < 2^16
   auto source = [&](int i, int &n) {
-    n = toks[i / a.G];
-    return qbase + static_cast<int64_t>(i % a.G) * a.Nq + n;
+    const int q = a.G == 1 ? i : static_cast<int>(__umulhi(i, per));
+    n = toks[q];
+    return qbase + static_cast<int64_t>(i - q * a.G) * a.Nq + n;
   };
 
   if (warp >= 9) {
@@ -865,25 +902,24 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
       const SmemDesc ot = make_desc_sw128(smem_u32(sQ), kTcRows * 128, 1024);
       const SmemDesc qt = make_desc_sw128(smem_u32(sQ) + QT, kTcRows * 128, 1024);
       const SmemDesc pd = make_desc_sw128(smem_u32(sP), PT, 1024), gd = make_desc_sw128(smem_u32(sG), PT, 1024);
-      auto issue_s = [&](int t) {
-        const int st = t & 1;
-        if (!tc_wait(&B->q_full[st], (t >> 1) & 1, ns)) return false;
-        fence_proxy_async_smem();
-        tc_fence_after();
-        const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, SmemDesc{qd.lo + off, qd.hi},
-                                                                kd, IDESC_S, 0u);
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + st * kBaTile,
-                                                                SmemDesc{od.lo + off, od.hi}, vd, IDESC_S, 0u);
-        mma_commit(&B->s_full[st]);
-        return true;
-      };
-      bool ok = steps == 0 || issue_s(0);
-      for (int t = 0; t < steps && ok; ++t) {
-        const int st = t & 1;
-        // step t + 1's buffers were read before P(t - 1) was announced
-        if (t + 1 < steps && !issue_s(t + 1)) break;
-        if (!tc_wait(&B->p_full, t & 1, ns)) break;
+      for (int n_s = 0, t = 0; t < steps;) {
+        const int ss = n_s & 1, st = t & 1;
+        // step t + 1's score buffers were read before P(t - 1) was announced
+        const int next = tc_either(&B->q_full[ss], (n_s >> 1) & 1, n_s < steps && n_s <= t + 1, &B->p_full, t & 1,
+                                   t < n_s, ns);
+        if (next == 0) break;
+        if (next == 1) {
+          fence_proxy_async_smem();
+          tc_fence_after();
+          const uint32_t off = static_cast<uint32_t>(ss * 2 * QT) >> 4;
+          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + ss * kBaTile,
+                                                                  SmemDesc{qd.lo + off, qd.hi}, kd, IDESC_S, 0u);
+          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + ss * kBaTile,
+                                                                  SmemDesc{od.lo + off, od.hi}, vd, IDESC_S, 0u);
+          mma_commit(&B->s_full[ss]);
+          ++n_s;
+          continue;
+        }
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
         const uint32_t more = t > 0 ? 1u : 0u;
@@ -895,7 +931,7 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
                                                                   IDESC_G, more);
         mma_commit(&B->q_empty[st]);
         mma_commit(&B->p_free);
-        if (t == steps - 1) mma_commit(&B->done);
+        if (++t == steps) mma_commit(&B->done);
       }
       mma_commit(&B->drain);
       mbar_wait(&B->drain, 0, 1000000000ull);
