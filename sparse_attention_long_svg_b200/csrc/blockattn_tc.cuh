@@ -71,22 +71,6 @@ __device__ __forceinline__ void tc_load_rows(uint32_t dst, const __nv_bfloat16 *
   }
 }
 
-// Which of two chains the issuing thread can go on with: 1 when `a` has
-// completed (and is wanted), else 2 when `b` has, 0 after `ns`.  A chain whose
-// operands are late must not hold up the other, which frees their buffers.
-__device__ __forceinline__ int tc_either(uint64_t *a, uint32_t pa, bool want_a, uint64_t *b, uint32_t pb, bool want_b,
-                                         uint64_t ns) {
-  const long long t0 = clock64(), limit = static_cast<long long>(ns) * 2;
-  while (true) {
-    if (want_a && mbar_test(a, pa)) return 1;
-    if (want_b && mbar_test(b, pb)) return 2;
-    if (clock64() - t0 > limit) {
-      record_error(SVG_ERR_TIMEOUT, SVG_SITE_BLOCK_ATTN);
-      return 0;
-    }
-  }
-}
-
 struct TcBars {                       // at most 192 bytes
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], done, drain;
   uint32_t tmem;
@@ -275,24 +259,26 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
       const SmemDesc qd = make_desc_sw128(smem_u32(smem), 16, 1024);
       const SmemDesc kd = make_desc_sw128(smem_u32(sKV), 16, 1024);
       const SmemDesc vd = make_desc_sw128(smem_u32(sKV) + KV, kBaTile * 128, 1024);
-      for (int ns_done = 0, t = 0; t < steps;) {      // score products issued, value products issued
-        const int ss = ns_done & 1, st = t & 1;
-        // S(t + 1) goes before P(t) V; its buffer held P(t - 1), whose product was issued before
-        const int next = tc_either(&B->k_full[ss], (ns_done >> 1) & 1, ns_done < steps && ns_done <= t + 1,
-                                   &B->p_full[st], (t >> 1) & 1, t < ns_done, ns);
-        if (next == 0) break;
-        if (next == 1) {
-          fence_proxy_async_smem();                 // cp.async writes -> tensor-core reads
-          tc_fence_after();
-          const uint32_t off = static_cast<uint32_t>(ss * 2 * KV) >> 4;
-          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + ss * kBaTile, qd,
-                                                                  SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
-          mma_commit(&B->s_full[ss]);
-          mma_commit(&B->k_empty[ss]);
-          ++ns_done;
-          continue;
-        }
-        if (!tc_wait(&B->v_full[st], (t >> 1) & 1, ns)) break;
+      int n_s = 0;                                  // score products issued
+      auto issue_s = [&]() {
+        const int st = n_s & 1;
+        if (!tc_wait(&B->k_full[st], (n_s >> 1) & 1, ns)) return false;
+        fence_proxy_async_smem();                   // cp.async writes -> tensor-core reads
+        tc_fence_after();
+        const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, qd,
+                                                                SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
+        mma_commit(&B->s_full[st]);
+        mma_commit(&B->k_empty[st]);
+        ++n_s;
+        return true;
+      };
+      bool ok = steps == 0 || issue_s();
+      for (int t = 0; t < steps && ok; ++t) {
+        const int st = t & 1;
+        // its score buffer held P(t-1), whose product was issued before
+        if (t + 1 < steps && !issue_s()) break;
+        if (!tc_wait(&B->v_full[st], (t >> 1) & 1, ns) || !tc_wait(&B->p_full[st], (t >> 1) & 1, ns)) break;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
@@ -303,7 +289,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
                       t > 0 || k > 0 ? 1u : 0u);
         mma_commit(&B->v_empty[st]);
         mma_commit(&B->done);
-        ++t;
       }
       mma_commit(&B->drain);                        // all retired before TMEM is released
       mbar_wait(&B->drain, 0, 1000000000ull);
@@ -628,30 +613,30 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
       const SmemDesc kd = make_desc_sw128(smem_u32(sK), 16, 1024);
       const SmemDesc vd = make_desc_sw128(smem_u32(sV), 16, 1024);
       const SmemDesc kn = make_desc_sw128(smem_u32(sK), kBaTile * 128, 1024);
-      int st = 0, ph = 0, done = 0;                 // stage of the next scores, of the next dQ product
-      for (int n_s = 0, t = 0; t < steps;) {
-        // S and dP of step t + 1 go before dQ(t); their buffers held dS(t - 1), whose product was issued before
-        const int next = tc_either(&B->k_full[st], ph, n_s < steps && n_s <= t + 1, &B->ds_full[t & 1], (t >> 1) & 1,
-                                   t < n_s, ns);
-        if (next == 0) break;
-        if (next == 1) {
-          if (!tc_wait(&B->v_full[st], ph, ns)) break;
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint32_t off = static_cast<uint32_t>(st * KV) >> 4, buf = (n_s & 1) * kBaTile;
-          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + buf, qd, SmemDesc{kd.lo + off, kd.hi},
-                                                                  IDESC_S, 0u);
-          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + buf, od, SmemDesc{vd.lo + off, vd.hi},
-                                                                  IDESC_S, 0u);
-          mma_commit(&B->s_full[n_s & 1]);
-          mma_commit(&B->v_empty[st]);
-          ++n_s;
-          if (++st == NS) {
-            st = 0;
-            ph ^= 1;
-          }
-          continue;
+      int st = 0, ph = 0, done = 0, n_s = 0;        // stages of the next scores and dQ product; scores issued
+      auto issue_s = [&]() {                        // S and dP, into the buffers of the step's group
+        if (!tc_wait(&B->k_full[st], ph, ns) || !tc_wait(&B->v_full[st], ph, ns)) return false;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t off = static_cast<uint32_t>(st * KV) >> 4, buf = (n_s & 1) * kBaTile;
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + buf, qd, SmemDesc{kd.lo + off, kd.hi},
+                                                                IDESC_S, 0u);
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + buf, od, SmemDesc{vd.lo + off, vd.hi},
+                                                                IDESC_S, 0u);
+        mma_commit(&B->s_full[n_s & 1]);
+        mma_commit(&B->v_empty[st]);
+        ++n_s;
+        if (++st == NS) {
+          st = 0;
+          ph ^= 1;
         }
+        return true;
+      };
+      bool ok = steps == 0 || issue_s();
+      for (int t = 0; t < steps && ok; ++t) {
+        // the buffers of step t + 1 held dS(t - 1), whose product was issued before
+        if (t + 1 < steps && !issue_s()) break;
+        if (!tc_wait(&B->ds_full[t & 1], (t >> 1) & 1, ns)) break;
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(done * KV) >> 4;
 #pragma unroll
@@ -660,8 +645,8 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
                       (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + ((k * 2048) >> 4)), IDESC_DQ,
                       t > 0 || k > 0 ? 1u : 0u);
         mma_commit(&B->k_empty[done]);
+        if (t == steps - 1) mma_commit(&B->done);
         if (++done == NS) done = 0;
-        if (++t == steps) mma_commit(&B->done);
       }
       mma_commit(&B->drain);
       mbar_wait(&B->drain, 0, 1000000000ull);
@@ -902,24 +887,29 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
       const SmemDesc ot = make_desc_sw128(smem_u32(sQ), kTcRows * 128, 1024);
       const SmemDesc qt = make_desc_sw128(smem_u32(sQ) + QT, kTcRows * 128, 1024);
       const SmemDesc pd = make_desc_sw128(smem_u32(sP), PT, 1024), gd = make_desc_sw128(smem_u32(sG), PT, 1024);
-      for (int n_s = 0, t = 0; t < steps;) {
-        const int ss = n_s & 1, st = t & 1;
-        // step t + 1's score buffers were read before P(t - 1) was announced
-        const int next = tc_either(&B->q_full[ss], (n_s >> 1) & 1, n_s < steps && n_s <= t + 1, &B->p_full, t & 1,
-                                   t < n_s, ns);
-        if (next == 0) break;
-        if (next == 1) {
-          fence_proxy_async_smem();
-          tc_fence_after();
-          const uint32_t off = static_cast<uint32_t>(ss * 2 * QT) >> 4;
-          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + ss * kBaTile,
-                                                                  SmemDesc{qd.lo + off, qd.hi}, kd, IDESC_S, 0u);
-          mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + ss * kBaTile,
-                                                                  SmemDesc{od.lo + off, od.hi}, vd, IDESC_S, 0u);
-          mma_commit(&B->s_full[ss]);
-          ++n_s;
-          continue;
-        }
+      int n_s = 0;                                  // steps whose scores are issued
+      auto issue_s = [&]() {
+        const int st = n_s & 1;
+        if (!tc_wait(&B->q_full[st], (n_s >> 1) & 1, ns)) return false;
+        fence_proxy_async_smem();
+        tc_fence_after();
+        const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, SmemDesc{qd.lo + off, qd.hi},
+                                                                kd, IDESC_S, 0u);
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + st * kBaTile,
+                                                                SmemDesc{od.lo + off, od.hi}, vd, IDESC_S, 0u);
+        mma_commit(&B->s_full[st]);
+        ++n_s;
+        return true;
+      };
+      for (int t = 0; t < steps; ++t) {
+        const int st = t & 1;
+        // Scores of step t + 1 first (their buffers were read before P(t - 1)
+        // was announced), unless its rows are still on their way: step t's
+        // products, which free a stage, must not wait for them.
+        if (n_s == t && !issue_s()) break;
+        if (t + 1 < steps && mbar_test(&B->q_full[st ^ 1], ((t + 1) >> 1) & 1) && !issue_s()) break;
+        if (!tc_wait(&B->p_full, t & 1, ns)) break;
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
         const uint32_t more = t > 0 ? 1u : 0u;
@@ -931,7 +921,7 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
                                                                   IDESC_G, more);
         mma_commit(&B->q_empty[st]);
         mma_commit(&B->p_free);
-        if (++t == steps) mma_commit(&B->done);
+        if (t == steps - 1) mma_commit(&B->done);
       }
       mma_commit(&B->drain);
       mbar_wait(&B->drain, 0, 1000000000ull);
