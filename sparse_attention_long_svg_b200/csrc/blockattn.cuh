@@ -67,43 +67,17 @@ __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int
   // reciprocal adds less than 2^-14
   const uint32_t per = 0xFFFFFFFFu / a.topk + 1;
   __syncthreads();
-  if (tokens >= 64) {
-    // a thread to a token: it owns its words, so that bits gather in a register
-    // until the word changes (ids mostly ascend), without atomics
-    if (tid < tokens && n0 + tid < a.Nq) {
-      const int seen = query_seen(a, len, n0 + tid);
-      int at = -1;
-      uint32_t word = 0;
-      for (int i0 = 0; i0 < a.topk; i0 += 2 * U) {
-        int j[2 * U];
+  for (int i0 = tid; i0 < ids; i0 += U * threads) {
+    int j[U];
 #pragma unroll
-        for (int u = 0; u < 2 * U; ++u) j[u] = __ldg(sel + tid * a.topk + min(i0 + u, a.topk - 1));
+    for (int u = 0; u < U; ++u) j[u] = __ldg(sel + min(i0 + u * threads, ids - 1));
 #pragma unroll
-        for (int u = 0; u < 2 * U; ++u) {           // the last id again, past the end, does no harm
-          if (j[u] < 0 || j[u] >= a.nblk || static_cast<int64_t>(j[u]) * a.block >= seen) continue;
-          if ((j[u] >> 5) != at) {
-            if (at >= 0) bits[at * tokens + tid] |= word;
-            at = j[u] >> 5;
-            word = 0;
-          }
-          word |= 1u << (j[u] & 31);
-        }
-      }
-      if (at >= 0) bits[at * tokens + tid] |= word;
-    }
-  } else {
-    for (int i0 = tid; i0 < ids; i0 += U * threads) {
-      int j[U];
-  #pragma unroll
-      for (int u = 0; u < U; ++u) j[u] = __ldg(sel + min(i0 + u * threads, ids - 1));
-  #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + u * threads;
-        if (i >= ids) break;
-        const int tok = a.topk == 1 ? i : static_cast<int>(__umulhi(i, per));
-        if (j[u] >= 0 && j[u] < a.nblk && static_cast<int64_t>(j[u]) * a.block < query_seen(a, len, n0 + tok))
-          atomicOr(&bits[(j[u] >> 5) * tokens + tok], 1u << (j[u] & 31));
-      }
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * threads;
+      if (i >= ids) break;
+      const int tok = a.topk == 1 ? i : static_cast<int>(__umulhi(i, per));
+      if (j[u] >= 0 && j[u] < a.nblk && static_cast<int64_t>(j[u]) * a.block < query_seen(a, len, n0 + tok))
+        atomicOr(&bits[(j[u] >> 5) * tokens + tok], 1u << (j[u] & 31));
     }
   }
   __syncthreads();

@@ -274,13 +274,11 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
     f[i] = none;
     if (i * 32 + lane < r.may) f[i] = s[i * 32 + lane];
   }
-  // NaN counts as -inf; the places with forced blocks are the first and the last few
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
-    if (i * 32 >= r.may) break;
-    f[i] = i * 32 + lane < r.may ? fmaxf(f[i], -INFINITY) : none;
-    if (i * 32 < r.s1 || (i * 32 < r.l1 && i * 32 + 31 >= r.l0))
-      if (r.forced(i * 32 + lane)) f[i] = none;
+    const int j = i * 32 + lane;
+    // NaN counts as -inf
+    f[i] = j < r.s1 || (j >= r.l0 && j < r.l1) || j >= r.may ? none : fmaxf(f[i], -INFINITY);
     mine = fmaxf(mine, f[i]);
   }
   float hi = unkey32(__reduce_max_sync(all, key32(mine)));
@@ -292,38 +290,43 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
     lo = unkey32(__reduce_min_sync(all, key32(mine)));
   }
   if (need == 0 || !(hi - lo < 3.0e38f)) return false;
-  auto count = [&](float x) {
-    float c0 = 0.f, c1 = 0.f;                       // a comparison yields 1.0f in one instruction
+  // Bisection between lo (at least `need` are not below it) and hi (one is not,
+  // unless equal).  A comparison yields 1.0f in one instruction.
+  float mid = hi;
+  while (true) {
+    float c0 = 0.f, c1 = 0.f;
 #pragma unroll
     for (int i = 0; i < VPL; i += 2) {
-      if (i % 8 == 0 && i * 32 >= r.may) break;
-      c0 += f[i] >= x ? 1.f : 0.f;
-      c1 += f[i + 1] >= x ? 1.f : 0.f;
+      if (VPL > 16 && i % 16 == 0 && i * 32 >= r.may) break;
+      c0 += f[i] >= mid ? 1.f : 0.f;
+      c1 += f[i + 1] >= mid ? 1.f : 0.f;
     }
-    return __reduce_add_sync(all, static_cast<int>(c0 + c1));
-  };
-  // at least `need` are not below lo; fewer not below hi, unless lo == hi
-  if (count(hi) >= need) lo = hi;
-  while (lo < hi) {
-    const float mid = lo + 0.5f * (hi - lo);
-    if (!(mid > lo && mid < hi)) break;             // neighbours: equal scores
-    const int c = count(mid);
+    const int c = __reduce_add_sync(all, static_cast<int>(c0 + c1));
     if (c >= need) lo = mid;
     else hi = mid;
     if (c == need) break;
+    mid = lo + 0.5f * (hi - lo);
+    if (!(mid > lo && mid < hi)) break;             // equal, or neighbours: equal scores
   }
-  // the last place's score, and who is near it
+  // the last place's score, and who is near it or above: bit i of a lane's words
   float least = INFINITY;
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
     if (f[i] >= lo) least = fminf(least, f[i]);
   const float t = unkey32(__reduce_min_sync(all, key32(least)));
   const float over = t + 2.f * bound, under = t - 2.f * bound;
+  constexpr int WORDS = (VPL + 31) / 32;
+  uint32_t cand[WORDS], sure_bits[WORDS];
   int both = 0;                                     // near ones above 2^16, above ones below
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    if (i % 8 == 0 && i * 32 >= r.may) break;
-    both += f[i] > over ? 1 : f[i] >= under ? 1 << 16 : 0;
+  for (int w = 0; w < WORDS; ++w) {
+    cand[w] = sure_bits[w] = 0;
+#pragma unroll
+    for (int i = 32 * w; i < min(VPL, 32 * w + 32); ++i) {
+      cand[w] |= f[i] >= under ? 1u << (i & 31) : 0u;
+      sure_bits[w] |= f[i] > over ? 1u << (i & 31) : 0u;
+    }
+    both += __popc(sure_bits[w]) + (__popc(cand[w] & ~sure_bits[w]) << 16);
   }
   both = __reduce_add_sync(all, both);
   const int sure = both & 0xFFFF, nears = both >> 16;
@@ -332,12 +335,14 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
     if (nears > 32 || !(bound < INFINITY)) return false;
     int at = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (i * 32 >= r.may) break;
-      const bool near = f[i] >= under && !(f[i] > over);
-      const uint32_t m = __ballot_sync(all, near);
-      if (near) near_list[at + __popc(m & below)] = i * 32 + lane;
-      at += __popc(m);
+    for (int w = 0; w < WORDS; ++w) {
+      const uint32_t near = cand[w] & ~sure_bits[w];
+      for (uint32_t places = __reduce_or_sync(all, near); places; places &= places - 1) {
+        const int i = __ffs(places) - 1;
+        const uint32_t m = __ballot_sync(all, (near >> i) & 1u);
+        if ((near >> i) & 1u) near_list[at + __popc(m & below)] = (32 * w + i) * 32 + lane;
+        at += __popc(m);
+      }
     }
     __syncwarp();
     stay = rank_near<D>(a, near_list, nears, need - sure, head, n);
@@ -345,21 +350,19 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
   int seen = 0, at = 0, low = 0;
   const int l0 = max(r.l0, r.s1);
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    if (i * 32 >= r.may) break;
-    const uint32_t cand = __ballot_sync(all, f[i] >= under);
-    if (cand == 0) continue;
-    const uint32_t nm = cand & ~__ballot_sync(all, f[i] > over);
-    const int mine_near = seen + __popc(nm & below);
-    const bool in = ((cand >> lane) & 1u) && (!((nm >> lane) & 1u) || ((stay >> (mine_near & 31)) & 1u));
-    seen += __popc(nm);
-    const uint32_t m = __ballot_sync(all, in);
-    const int j = i * 32 + lane;
-    // before it: forced blocks below it and kept ones
-    if (in) out[at + __popc(m & below) + r.s1 + max(0, min(j, r.l1) - l0)] = j;
-    at += __popc(m);
-    low += __popc(__ballot_sync(all, in && j < l0));
-  }
+  for (int w = 0; w < WORDS; ++w)
+    for (uint32_t places = __reduce_or_sync(all, cand[w]); places; places &= places - 1) {
+      const int i = __ffs(places) - 1, j = (32 * w + i) * 32 + lane;
+      const bool is = (cand[w] >> i) & 1u, near = is && !((sure_bits[w] >> i) & 1u);
+      const uint32_t nm = __ballot_sync(all, near);
+      const bool in = is && (!near || ((stay >> ((seen + __popc(nm & below)) & 31)) & 1u));
+      const uint32_t m = __ballot_sync(all, in);
+      seen += __popc(nm);
+      // before it: forced blocks below it and kept ones
+      if (in) out[at + __popc(m & below) + r.s1 + max(0, min(j, r.l1) - l0)] = j;
+      at += __popc(m);
+      if ((32 * w + i) * 32 < l0) low += __popc(__ballot_sync(all, in && j < l0));
+    }
   for (int i = lane; i < r.s1; i += 32) out[i] = i;
   for (int i = l0 + lane; i < r.l1; i += 32) out[low + r.s1 + i - l0] = i;
   return true;
