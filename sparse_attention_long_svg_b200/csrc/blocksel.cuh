@@ -251,10 +251,9 @@ __device__ __noinline__ uint32_t rank_near(const SelectArgs &a, const int *near,
 //
 // The ordinary one keeps the row in registers (VPL places; forced blocks and
 // places without one are NaN, which no comparison takes) and finds the last
-// place's score by bisection, from the largest score down to a lower bound of
-// it: the smallest of the lanes' largest scores while topk <= 32, else the
-// smallest score.  Returns false, with nothing written, for rows that are flat
-// (more than 32 near the border) or hold infinities.
+// place's score from the lanes' largest ones (up to 32 places), or by bisection.
+// Returns false, with nothing written, for rows that are flat (more than 32
+// near the border) or hold infinities.
 template <int D, int VPL>
 __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, int *near_list, float bound, int head,
                                            int n, const SelectRange &r) {
@@ -281,39 +280,65 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
     f[i] = j < r.s1 || (j >= r.l0 && j < r.l1) || j >= r.may ? none : fmaxf(f[i], -INFINITY);
     mine = fmaxf(mine, f[i]);
   }
-  float hi = unkey32(__reduce_max_sync(all, key32(mine)));
-  float lo = unkey32(__reduce_min_sync(all, key32(mine)));
-  if (lo == -INFINITY || need > 32) {               // a lane without a candidate
-    mine = INFINITY;
+  if (need == 0) return false;
+  // the lanes' largest scores in descending order
+  float best = mine;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) mine = fminf(mine, f[i]);
-    lo = unkey32(__reduce_min_sync(all, key32(mine)));
-  }
-  if (need == 0 || !(hi - lo < 3.0e38f)) return false;
-  // Bisection between lo (at least `need` are not below it) and hi (one is not,
-  // unless equal).  A comparison yields 1.0f in one instruction.
-  float mid = hi;
-  while (true) {
-    float c0 = 0.f, c1 = 0.f;
+  for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
-    for (int i = 0; i < VPL; i += 2) {
-      if (VPL > 16 && i % 16 == 0 && i * 32 >= r.may) break;
-      c0 += f[i] >= mid ? 1.f : 0.f;
-      c1 += f[i + 1] >= mid ? 1.f : 0.f;
+    for (int o = k >> 1; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(all, best, o);
+      best = ((lane & k) == 0) == ((lane & o) == 0) ? fmaxf(best, x) : fminf(best, x);
     }
-    const int c = __reduce_add_sync(all, static_cast<int>(c0 + c1));
-    if (c >= need) lo = mid;
-    else hi = mid;
-    if (c == need) break;
-    mid = lo + 0.5f * (hi - lo);
-    if (!(mid > lo && mid < hi)) break;             // equal, or neighbours: equal scores
-  }
-  // the last place's score, and who is near it or above: bit i of a lane's words
-  float least = INFINITY;
+  const float top = __shfl_sync(all, best, 0);
+  // The need-th of them is a lower bound of the last place's score, and close:
+  // a few steps up, from one score to the next, reach it.
+  float t = __shfl_sync(all, best, min(need, 32) - 1);
+  bool found = false;
+  if (need <= 32 && t > -INFINITY)
+    for (int round = 0; round < 8; ++round) {
+      float c0 = 0.f, c1 = 0.f, next = INFINITY;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (f[i] >= lo) least = fminf(least, f[i]);
-  const float t = unkey32(__reduce_min_sync(all, key32(least)));
+      for (int i = 0; i < VPL; i += 2) {
+        if (VPL > 16 && i % 16 == 0 && i * 32 >= r.may) break;
+        c0 += f[i] > t ? 1.f : 0.f;                 // a comparison yields 1.0f in one instruction
+        c1 += f[i + 1] > t ? 1.f : 0.f;
+        next = fminf(next, fminf(f[i] > t ? f[i] : INFINITY, f[i + 1] > t ? f[i + 1] : INFINITY));
+      }
+      found = __reduce_add_sync(all, static_cast<int>(c0 + c1)) < need;
+      if (found) break;
+      t = unkey32(__reduce_min_sync(all, key32(next)));
+    }
+  if (!found) {
+    // bisection between lo (at least `need` are not below it) and hi (one is not, unless equal)
+    float lo = INFINITY, hi = top;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) lo = fminf(lo, f[i]);
+    lo = unkey32(__reduce_min_sync(all, key32(lo)));
+    if (!(hi - lo < 3.0e38f)) return false;
+    float mid = hi;
+    while (true) {
+      float c0 = 0.f, c1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPL; i += 2) {
+        if (VPL > 16 && i % 16 == 0 && i * 32 >= r.may) break;
+        c0 += f[i] >= mid ? 1.f : 0.f;
+        c1 += f[i + 1] >= mid ? 1.f : 0.f;
+      }
+      const int c = __reduce_add_sync(all, static_cast<int>(c0 + c1));
+      if (c >= need) lo = mid;
+      else hi = mid;
+      if (c == need) break;
+      mid = lo + 0.5f * (hi - lo);
+      if (!(mid > lo && mid < hi)) break;           // equal, or neighbours: equal scores
+    }
+    float least = INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (f[i] >= lo) least = fminf(least, f[i]);
+    t = unkey32(__reduce_min_sync(all, key32(least)));
+  }
+  // who is near the last place's score, t, or above: bit i of a lane's words
   const float over = t + 2.f * bound, under = t - 2.f * bound;
   constexpr int WORDS = (VPL + 31) / 32;
   uint32_t cand[WORDS], sure_bits[WORDS];

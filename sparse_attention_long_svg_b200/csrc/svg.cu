@@ -993,8 +993,10 @@ svg_status block_shapes(int BHq, int BHk, int B, int Nq, int Nk, int D, int bloc
 bool select_few(int Nq) { return Nq <= 4; }
 int64_t select_items(int BHk, int Nq) { return static_cast<int64_t>(BHk) * ((Nq + kSelTile - 1) / kSelTile); }
 // Items of a part: a multiple of what runs at a time (3 per SM) whose scores take
-// at most 64 MiB, half of L2.
-constexpr int64_t kSelPartBytes = 64ll << 20;
+// at most 256 MiB.  32,760 queries x 8 key heads x 512 blocks: 64 MiB, which
+// stay in L2, 883 us; 128 MiB 816 us; 256 MiB 768 us (fewer launches with a
+// tail each).
+constexpr int64_t kSelPartBytes = 256ll << 20;
 int64_t select_part(int BHk, int Nq, int nblk) {
   const int64_t row = (nblk + kSelTile - 1) / kSelTile * kSelTile * sizeof(float);
   const int64_t wave = 3ll * num_sms();
