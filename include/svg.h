@@ -461,7 +461,9 @@ svg_status svg_get_error_detail(svg_stream_t stream, int32_t *site, int32_t *blo
  * the following svg_sparse_attn launches skip loading their query tiles, so
  * the kernel's bounded waits run out, it records SVG_ERR_TIMEOUT, waits for
  * its own in-flight copies, frees its tensor memory and returns; fault = 0
- * restores normal operation.  Outputs of a faulted launch are undefined. */
+ * restores normal operation.  Outputs of a faulted launch are undefined.  The
+ * many-query kernels of svg_block_attn and svg_block_attn_backward skip their
+ * K and V (query row) loads in the same way. */
 void svg_debug_set_fault(int fault);
 
 /* ------------------------------------------------------------------------ kernel timing

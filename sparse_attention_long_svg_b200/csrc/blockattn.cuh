@@ -45,6 +45,7 @@ struct BlockAttnArgs {
   int item_tokens, tile_tokens;
   float scale, scale_log2;
   uint64_t wait_ns;
+  int fault;                           // test hook: K and V (the gathered rows) are not loaded
 };
 
 // Keys the query n sees.

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
     // ---------------------------------------------------------------- loads: K, V
     const bool is_v = warp == 6;
     uint64_t *full = is_v ? B->v_full : B->k_full, *empty = is_v ? B->v_empty : B->k_empty;
-    for (int t = 0; t < steps; ++t) {
+    for (int t = 0; t < steps && !a.fault; ++t) {
       const int st = t & 1;
       if (t >= 2 && !tc_warp_wait(&empty[st], ((t >> 1) - 1) & 1, ns)) break;
       tc_load_tile<D>(smem_u32(sKV) + static_cast<uint32_t>(2 * st + is_v) * KV, is_v ? vh : kh, un.key(un.u0 + t), len);
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
     const bool is_v = warp == 10;
     uint64_t *full = is_v ? B->v_full : B->k_full, *empty = is_v ? B->v_empty : B->k_empty;
     int st = 0, ph = 1;                             // the first round finds the stages empty
-    for (int t = 0; t < steps; ++t) {
+    for (int t = 0; t < steps && !a.fault; ++t) {
       if (t >= NS && !tc_warp_wait(&empty[st], ph, ns)) break;
       tc_load_tile<D>(smem_u32(is_v ? sV : sK) + static_cast<uint32_t>(st) * KV, is_v ? vh : kh, un.key(t), len);
       cp_async_arrive(&full[st]);
@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
     // ---------------------------------------------------------------- loads: 32 rows a warp
     constexpr int COLS16 = D / 8, PER = 32 / COLS16;
     const int base_row = (warp - 9) * 32, c = lane % COLS16;
-    for (int t = 0; t < steps; ++t) {
+    for (int t = 0; t < steps && !a.fault; ++t) {
       const int st = t & 1;
       if (t >= 2 && !tc_warp_wait(&B->q_empty[st], ((t >> 1) - 1) & 1, ns)) break;
       const int i = t * kTcRows + base_row + lane;

@@ -886,6 +886,8 @@ svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void 
     if (!y[t] || !aligned(y[t], 16) || y[t] == x[t]) return SVG_ERR_INVALID_ARG;
     if (t > 0 && !start && cap < N) return SVG_ERR_INVALID_ARG;
     a.y[t] = static_cast<__nv_bfloat16 *>(y[t]);
+    for (int u = 0; u < t; ++u)
+      if (a.heads[u] != 0 && y[u] == y[t]) return SVG_ERR_INVALID_ARG;
   }
   if (cos && !start && P < N) return SVG_ERR_INVALID_ARG;
   // One head per thread while that leaves the GPU short of threads, else 4 in
@@ -941,6 +943,8 @@ svg_status svg_qk_norm_rope_backward(const void *dq_out, const void *dk_out, con
     if (!dy[t] || !dx[t] || !aligned(dy[t], 16) || !aligned(dx[t], 16) || !rope_strides_ok(ds[t]))
       return SVG_ERR_INVALID_ARG;
     if (dx[t] == dy[t]) return SVG_ERR_INVALID_ARG;
+    for (int u = 0; u < t; ++u)
+      if (a.heads[u] != 0 && dx[u] == dx[t]) return SVG_ERR_INVALID_ARG;
     if (t > 0 && !start && cap < N) return SVG_ERR_INVALID_ARG;
     a.dy[t] = static_cast<const __nv_bfloat16 *>(dy[t]);
     a.dx[t] = static_cast<__nv_bfloat16 *>(dx[t]);
@@ -1111,6 +1115,7 @@ void block_attn_args(BlockAttnArgs &a, const void *q, const void *k, const void 
   a.scale = scale > 0.f ? scale : 1.f / std::sqrt(static_cast<float>(D));
   a.scale_log2 = a.scale * 1.4426950408889634f;
   a.wait_ns = g_wait_ns;
+  a.fault = g_fault;
 }
 }  // namespace
 

@@ -126,21 +126,24 @@ def test_the_library_refuses_bad_arguments_before_any_launch():
     st = (ctypes.c_int64 * 3)(64, 64, 64)
     bad = (ctypes.c_int64 * 3)(64, 65, 64)
 
+    vo = ctypes.c_void_p(0x50000)
+
     def rope(q=f, qs=st, qo=g, cos=f, sin=f, P=8, B=1, N=8, Hq=1, D=64, eps=1e-6, il=1, start=nul, ko=h, cap=8):
         return lib.svg_qk_norm_rope(q, qs, f, st, f, st, nul, nul, cos, sin, P, B, N, Hq, 1, D, eps, il, start, qo, ko,
-                                    h, cap, nul)
+                                    vo, cap, nul)
 
     assert rope(q=nul) == 1 and rope(qo=nul) == 1 and rope(qs=bad) == 1 and rope(q=odd) == 1 and rope(qo=f) == 1
     assert rope(cos=nul) == 1 and rope(P=7) == 1 and rope(B=0) == 1 and rope(N=0) == 1 and rope(cap=7) == 1
     assert rope(D=96) == 2 and rope(eps=-1.0) == 1 and rope(eps=float("nan")) == 1 and rope(il=2) == 1
+    assert rope(ko=vo) == 1 and rope(ko=g) == 1 and rope(start=f, cap=0) == 1
     assert rope(ko=nul) == 1 and rope(B=1 << 20, N=1 << 12, P=1 << 12, cap=1 << 12) == 2
 
-    def rope_back(ws=1 << 20, dq=h, dqs=st, D=64, dqo=g):
+    def rope_back(ws=1 << 20, dq=h, dqs=st, D=64, dqo=g, dk=ctypes.c_void_p(0x60000)):
         return lib.svg_qk_norm_rope_backward(dqo, g, g, f, st, f, st, nul, nul, f, f, 8, 1, 8, 1, 1, D, 1e-6, 1, nul, 8,
-                                             dq, dqs, h, st, h, st, nul, nul, f, ws, nul)
+                                             dq, dqs, dk, st, vo, st, nul, nul, f, ws, nul)
 
     assert rope_back(ws=0) == 3 and rope_back(dq=nul) == 1 and rope_back(dqs=bad) == 1 and rope_back(D=32) == 2
-    assert rope_back(dq=g) == 1 and rope_back(dqo=nul) == 1
+    assert rope_back(dq=g) == 1 and rope_back(dqo=nul) == 1 and rope_back(dk=vo) == 1 and rope_back(dk=h) == 1
     assert lib.svg_qk_norm_rope_backward_workspace_size(0, 8, 1, 1, 64) == 0
 
     mean = lambda k=f, B=1, Nk=100, D=64, block=64, new=0: lib.svg_block_mean(k, 2, B, Nk, D, block, nul, new, g, nul)  # noqa: E731,E501

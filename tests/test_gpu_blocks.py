@@ -244,6 +244,9 @@ SELECT = [  # B, Hq, Hk, Nq, Nk, D, block, topk, sink, local, causal, lens
     (2, 10, 2, 1, 3000, 128, 64, 8, 1, 2, True, (3000, 1501)),
     (2, 4, 2, 4, 20000, 128, 64, 16, 2, 1, True, (20000, 9999)),
     (1, 2, 2, 3, 90000, 64, 64, 9, 0, 1, True, None),
+    (2, 2, 1, 5, 9000, 128, 64, 40, 3, 1, True, (9000, 2)),
+    (1, 4, 2, 129, 262144, 64, 64, 70, 2, 2, True, None),
+    (1, 1, 1, 130, 600, 128, 64, 3, 1, 2, True, None),
     (1, 5, 1, 200, 200, 128, 64, 2, 0, 1, True, None),
     (2, 6, 2, 333, 700, 64, 64, 5, 1, 2, True, (700, 300)),
     (1, 2, 1, 70, 5000, 128, 128, 6, 0, 0, False, None),
@@ -388,6 +391,111 @@ def test_what_a_query_does_not_list_does_not_reach_it(Nq):
     k2[1, 193], v2[1, 193] = k[1, 193], v[1, 193]
     g2 = svg.block_attn_backward(do, q, k2, v2, clean, lse, sel, 64, False, kv_len=kv)
     assert all(torch.equal(x, y) for x, y in zip(g, g2))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_that_outgrow_their_reference_and_keys_of_minus_infinity(D):
+    """Scores that rise by far more than the rescaling step from block to block, a key whose scores are all -inf,
+    and a query with no finite score."""
+    N, scale = 300, D ** -0.5
+    q, k, v = tokens(85, 1, 2, 1, N, N, D)
+    k[0] *= (1.0 + torch.arange(N, device="cuda") // 64 * 3)[:, None].to(BF)
+    q[0, 200] = 1.0
+    k[0, 70] = -float("inf")                        # -inf for that query, NaN or -inf for others
+    sel = torch.arange(5, dtype=torch.int32, device="cuda").expand(1, N, 5).contiguous()
+    o, lse = svg.block_attn(q, k, v, sel, 64, True, want_lse=True)
+    k[0, 70] = 0
+    s = (q[0, 200].float() @ k[0, :201].float().T) * scale
+    s[70] = -float("inf")
+    want = (s.double().softmax(0) @ v[0, :201].double())
+    assert (o[0, 200].double() - want).abs().max() <= 0.04 and abs(lse[0, 200] - s.double().logsumexp(0)) <= 1e-4
+    assert o[:, :70].isfinite().all()
+    o, lse = svg.block_attn(q, k, v, sel, 64, True, want_lse=True)
+    want, want_l, b, bl = bo.attention(f64(q), f64(k), f64(v), sel.cpu().numpy(), 64, True, [N], scale)
+    within(o, want, b)
+    within(lse, want_l, bl)
+
+
+def test_future_keys_that_are_not_finite_stay_in_the_future():
+    """Causal rows of a block whose later keys hold NaN and infinities (V and K): rows before them are clean."""
+    N, D = 150, 128
+    q, k, v = tokens(86, 1, 4, 2, N, N, D)
+    sel = torch.arange(3, dtype=torch.int32, device="cuda").expand(2, N, 3).contiguous()
+    clean, lse = svg.block_attn(q, k, v, sel, 64, True, want_lse=True)
+    do = bf(87, 4, N, D)
+    dq, _, _ = svg.block_attn_backward(do, q, k, v, clean, lse, sel, 64)
+    k2, v2 = k.clone(), v.clone()
+    v2[:, 100] = float("nan")
+    k2[0, 101] = float("inf")
+    v2[1, 30, 5] = float("inf")
+    o, lse2 = svg.block_attn(q, k2, v2, sel, 64, True, want_lse=True)
+    first = [100, 100, 30, 30]
+    for h, n in enumerate(first):
+        # a row computed again sums in another order: one rounding each
+        off = (o[h, :n].double() - clean[h, :n].double()).abs()
+        assert (off <= 2 * bo.HALF_BF16 * (clean[h, :n].double().abs() + v[h // 2].double().abs().max())).all()
+        assert (lse2[h, :n] - lse[h, :n]).abs().max() <= 1e-5 * (1 + lse.abs().max())
+        assert o[h, 101:].isnan().any(-1).all()
+    dq2, _, _ = svg.block_attn_backward(do, q, k2, v2, clean, lse, sel, 64)
+    for h, n in enumerate(first):
+        a, b = dq2[h, :n].double(), dq[h, :n].double()
+        assert a.isfinite().all() and (a - b).norm() <= 0.02 * b.norm()
+
+
+def test_a_sequence_of_4096_blocks():
+    """The longest list of blocks; its bit sets leave the gradient half a tile of tokens."""
+    Hq, Nq, Nk, D = 2, 150, 262144, 128
+    q, k, v = tokens(94, 1, Hq, Hq, Nq, Nk, D)
+    g = np.random.default_rng(95)
+    sel = torch.from_numpy(np.sort(g.integers(0, 4096, (Hq, Nq, 4)).astype(np.int32), -1)).cuda()
+    sel[:, :, 3] = 4095
+    o, lse = svg.block_attn(q, k, v, sel, 64, want_lse=True)
+    do = bf(98, Hq, Nq, D)
+    got = svg.block_attn_backward(do, q, k, v, o, lse, sel, 64)
+    dk, dv = torch.zeros_like(k, dtype=torch.float64), torch.zeros_like(v, dtype=torch.float64)
+    for h in range(Hq):
+        for n in range(0, Nq, 7):
+            keys = torch.cat([torch.arange(j * 64, (j + 1) * 64, device="cuda") for j in sel[h, n].unique()])
+            keys = keys[keys <= Nk - Nq + n]
+            kk, vv = k[h, keys].double(), v[h, keys].double()
+            s = kk @ q[h, n].double() * D ** -0.5
+            p = s.softmax(0)
+            assert abs(lse[h, n] - s.logsumexp(0)) <= 1e-4
+            assert ((o[h, n].double() - p @ vv).abs() <= 2.2 * bo.HALF_BF16 * (p @ vv.abs())).all()
+            ds = p * (vv @ do[h, n].double() - do[h, n].double() @ o[h, n].double())
+            assert ((got[0][h, n].double() - ds @ kk * D ** -0.5).abs()
+                    <= 3 * bo.HALF_BF16 * (ds.abs() @ kk.abs()) * D ** -0.5 + 1e-3).all()
+    # what nobody lists has no gradient
+    listed = torch.zeros(Hq, 4096, dtype=torch.bool, device="cuda").scatter_(1, sel.flatten(1).long(), True)
+    for x in got[1:]:
+        assert not x.view(Hq, 4096, 64 * D)[~listed].any() and x.view(Hq, 4096, 64 * D)[listed].any(-1).all()
+
+
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_library_usable():
+    """A host-set flag keeps the matrix kernels from loading K and V, so their bounded waits run out: they record it,
+    free their tensor memory and return (no GPU fault)."""
+    lib = svg.load_library()
+    N, D = 200, 128
+    q, k, v = tokens(88, 1, 4, 2, N, N, D)
+    sel = torch.arange(4, dtype=torch.int32, device="cuda").expand(2, N, 4).contiguous()
+    want, lse = svg.block_attn(q, k, v, sel, 64, want_lse=True)
+    grads = svg.block_attn_backward(q, q, k, v, want, lse, sel, 64)
+    torch.cuda.synchronize()
+    assert svg.get_error() == 0
+    try:
+        svg.set_wait_timeout_ns(20_000_000)
+        lib.svg_debug_set_fault(1)
+        svg.block_attn(q, k, v, sel, 64)
+        assert svg.get_error_detail()[:2] == (5, "block attention")
+        svg.block_attn_backward(q, q, k, v, want, lse, sel, 64)
+        assert svg.get_error_detail()[:2] == (5, "block attention")
+    finally:
+        lib.svg_debug_set_fault(0)
+        svg.set_wait_timeout_ns(0)
+    again, _ = svg.block_attn(q, k, v, sel, 64)
+    assert torch.equal(again, want) and svg.get_error() == 0
+    for x, y in zip(svg.block_attn_backward(q, q, k, v, want, lse, sel, 64), grads):
+        assert torch.equal(x, y)
 
 
 def test_offsets_beyond_32_bits():
