@@ -72,7 +72,7 @@ __device__ __forceinline__ void tc_load_rows(uint32_t dst, const __nv_bfloat16 *
 }
 
 struct TcBars {                       // at most 192 bytes
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], done, drain;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], done, last, drain;
   uint32_t tmem;
   int count;
 };
@@ -217,6 +217,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
       mbar_init(&B->p_full[i], 128);
     }
     mbar_init(&B->done, 1);
+    mbar_init(&B->last, 1);
     mbar_init(&B->drain, 1);
     fence_mbar_init();
   }
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
                       t > 0 || k > 0 ? 1u : 0u);
         mma_commit(&B->v_empty[st]);
         mma_commit(&B->done);
+        if (t == steps - 1) mma_commit(&B->last);
       }
       mma_commit(&B->drain);                        // all retired before TMEM is released
       mbar_wait(&B->drain, 0, 1000000000ull);
@@ -373,7 +375,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
       tc_fence_before();
       mbar_arrive(&B->p_full[st]);
     }
-    if (ok && steps > 0) ok = tc_warp_wait(&B->done, (steps - 1) & 1, ns);
+    // (`done` may still be two phases behind here, where its parity would tell nothing)
+    if (ok && steps > 0) ok = tc_warp_wait(&B->last, 0, ns);
     tc_fence_after();
     const bool none = m == -INFINITY && l == 0.f;
     const float inv = none ? 0.f : 1.f / l;

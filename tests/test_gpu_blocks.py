@@ -349,6 +349,43 @@ def test_attention_and_gradient(B, Hq, Hk, Nq, Nk, D, block, topk, causal, lens)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("G,D,causal", [(5, 128, True), (1, 64, False)])
+def test_many_tiles_at_once(G, D, causal):
+    """Hundreds of tiles that share the GPU, so that warps of a tile run apart: against dense attention in 64 bits, and
+    twice the same."""
+    Hk, N, topk = 4, 3000, 12
+    Hq = Hk * G
+    q, k, v = tokens(66, 1, Hq, Hk, N, N, D)
+    g = torch.Generator().manual_seed(67)
+    near = torch.arange(N)[None, :, None] // 64 - torch.arange(4)
+    sel = torch.cat([near.expand(Hk, N, 4), torch.randint(0, 47, (Hk, N, topk - 4), generator=g)], 2).int().cuda()
+    o, lse = svg.block_attn(q, k, v, sel, 64, causal, want_lse=True)
+    do = bf(69, Hq, N, D)
+    grads = svg.block_attn_backward(do, q, k, v, o, lse, sel, 64, causal)
+    for _ in range(3):
+        again = svg.block_attn(q, k, v, sel, 64, causal, want_lse=True)
+        assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+        for x, y in zip(svg.block_attn_backward(do, q, k, v, o, lse, sel, 64, causal), grads):
+            assert torch.equal(x, y)
+    hit = torch.zeros(Hk, N, 48, dtype=torch.bool, device="cuda")
+    hit.scatter_(2, torch.where(sel < 0, 47, sel).long(), True)
+    mask = hit[:, :, :47].repeat_interleave(64, 2)[:, :, :N]
+    if causal:
+        mask &= torch.arange(N, device="cuda") <= torch.arange(N, device="cuda")[:, None]
+    for h in range(Hq):
+        kk, vv = k[h // G].double(), v[h // G].double()
+        s = (q[h].double() @ kk.T * D ** -0.5).masked_fill(~mask[h // G], -float("inf"))
+        p = s.softmax(-1)
+        size = p @ vv.abs()
+        # half a bf16 step of the result and of the weights, and their sums
+        assert ((o[h].double() - p @ vv).abs() <= bo.HALF_BF16 * ((p @ vv).abs() + 1.1 * size)).all(), h
+        assert ((lse[h] - s.logsumexp(-1)).abs() <= 1e-4).all()
+        ds = p * (do[h].double() @ vv.T - (do[h].double() * o[h].double()).sum(-1, keepdim=True))
+        want = ds @ kk * D ** -0.5
+        bound = bo.HALF_BF16 * (want.abs() + 1.2 * (ds.abs() @ kk.abs()) * D ** -0.5)
+        assert ((grads[0][h].double() - want).abs() <= bound + 1e-4).all(), h
+
+
 def test_gradient_of_a_block_that_everyone_lists():
     """A block whose queries fill several work items: partial sums in fp32, joined in order."""
     Hq, Hk, N, D = 8, 2, 1100, 64
