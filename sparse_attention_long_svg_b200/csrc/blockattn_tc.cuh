@@ -643,9 +643,9 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(done * KV) >> 4;
 #pragma unroll
-        for (int k = 0; k < kBaTile / 16; ++k)
+        for (int k = 0; k < 2 * kBaTile / 16; ++k)  // dS's high parts, then the low ones
           mma_bf16_ts(tmem, tmem + TM_S + (t & 1) * kBaTile + 8 * k,
-                      (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + ((k * 2048) >> 4)), IDESC_DQ,
+                      (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + (((k & 3) * 2048) >> 4)), IDESC_DQ,
                       t > 0 || k > 0 ? 1u : 0u);
         mma_commit(&B->k_empty[done]);
         if (t == steps - 1) mma_commit(&B->done);
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
       }
       tc_fence_after();
       const bool any = __any_sync(0xffffffffu, end > 0), part = __any_sync(0xffffffffu, end > 0 && end < kBaTile);
-      float g[32];
+      float g[32], rest[32];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (any) {
@@ -689,15 +689,22 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
               d[e] = p * (dp[c + e] - delta);
               if (part) d[e] = 32 * h + c + e < end ? d[e] : 0.f;
             }
-            // dS as bf16 for the matrix product: 2^-8 relative to each
-            g[16 * h + (c >> 1)] = end > 0 ? __uint_as_float(pack_bf16x2(d[0], d[1])) : 0.f;
+            // dS as two bf16 parts (2^-16 relative): a row's dS add up to zero, so what the keys have in common
+            // cancels in dQ, and rounding to one part would leave 2.5 times the error
+            const uint32_t top = end > 0 ? pack_bf16x2(d[0], d[1]) : 0u;
+            g[16 * h + (c >> 1)] = __uint_as_float(top);
+            rest[16 * h + (c >> 1)] =
+                end > 0 ? __uint_as_float(pack_bf16x2(d[0] - __uint_as_float(top << 16),
+                                                      d[1] - __uint_as_float(top & 0xFFFF0000u)))
+                        : 0.f;
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) g[16 * h + c] = 0.f;
+          for (int c = 0; c < 16; ++c) g[16 * h + c] = rest[16 * h + c] = 0.f;
         }
       }
       tmem_st32(s_at, g);
+      tmem_st32(s_at + 32, rest);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&B->ds_full[grp]);
