@@ -42,7 +42,7 @@ struct BlockAttnArgs {
   int32_t *items;                      // key tile of every work item
   float *part_kv;                      // [slot][2][64][D]
   int BHk, G, heads_per_seq, Nq, Nk, nblk, block, topk, causal, splits;
-  int item_tokens, tile_tokens;
+  int item_tokens, tile_tokens, k_stages;
   float scale, scale_log2;
   uint64_t wait_ns;
   int fault;                           // test hook: K and V (the gathered rows) are not loaded

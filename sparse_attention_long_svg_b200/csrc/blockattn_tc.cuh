@@ -481,35 +481,53 @@ __device__ __noinline__ void dq_row_again(const TcUnion &un, const __nv_bfloat16
   }
 }
 
-// dQ, and delta for the second kernel.  As the forward kernel, but scores need
-// no running maximum, so two groups of four warps take the steps in turn (a TMEM
-// lane belongs to a thread of each): S and dP of a step lie in the group's
-// buffers, dS replaces S there as the A operand of the product with K.
-constexpr int kTcDqThreads = 11 * 32, kTcDqStages = 3;
+// 16 consecutive fp32 columns of this thread's TMEM lane, waited for inside the
+// same asm statement.
+__device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 
-struct TcDqBars {                      // at most 256 bytes
-  uint64_t k_full[kTcDqStages], k_empty[kTcDqStages], v_full[kTcDqStages], v_empty[kTcDqStages], s_full[2], ds_full[2],
-      done, drain;
+// dQ, and delta for the second kernel: 128 rows against their union, as in the
+// forward kernel.  A step is a chain (K, V -> S, dP -> dS -> dQ), and a list is
+// short beside a CTA's start-up, so everything is held once and two CTAs share
+// an SM: one's chain and start-up fill the other's gaps (one CTA with three
+// stages and two score buffers took 650 us where this takes 460: 8,190 tokens,
+// 40 / 8 heads, 16 blocks).  Warps 0-7: two groups, 32 keys of a step each (a
+// TMEM lane belongs to a thread of each); a group's dS replaces its own scores
+// there, as the A operand of the product with K; warp 8 issues, 9 and 10 load.
+constexpr int kTcDqThreads = 11 * 32;
+
+struct TcDqBars {                      // at most 128 bytes
+  uint64_t k_full[2], k_empty[2], v_full, v_empty, s_full, ds_full, done, drain;
   uint32_t tmem;
   int count;
 };
 
 template <int D>
-__host__ __device__ inline size_t tc_dq_smem(int tokens, int nblk) {
-  return 2ull * kTcRows * D * 2 + 2ull * kTcDqStages * kBaTile * D * 2 + 256 + kTcRows * 8 + mark_bytes(tokens, nblk);
+__host__ __device__ inline size_t tc_dq_smem(int k_stages, int tokens, int nblk) {
+  return 2ull * kTcRows * D * 2 + (1ull + k_stages) * kBaTile * D * 2 + 128 + mark_bytes(tokens, nblk);
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const BlockAttnArgs a) {
+__global__ void __launch_bounds__(kTcDqThreads, 2) block_attn_dq_tc_kernel(const BlockAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  constexpr int Q_BYTES = kTcRows * D * 2, KV = kBaTile * D * 2, NS = kTcDqStages, COLS = 512;
+  constexpr int Q_BYTES = kTcRows * D * 2, KV = kBaTile * D * 2, COLS = 256;
   constexpr uint32_t IDESC_S = idesc_bf16_f32(kTcRows, kBaTile, false, false);
   constexpr uint32_t IDESC_DQ = idesc_bf16_f32(kTcRows, D, false, true);
-  constexpr uint32_t TM_S = D, TM_DP = D + 2 * kBaTile;
-  uint8_t *sK = smem + 2 * Q_BYTES, *sV = sK + NS * KV;
-  TcDqBars *B = reinterpret_cast<TcDqBars *>(sV + NS * KV);
-  float *row_lse = reinterpret_cast<float *>(sV + NS * KV + 256), *row_delta = row_lse + kTcRows;
-  uint32_t *bits = reinterpret_cast<uint32_t *>(row_delta + kTcRows);
+  constexpr uint32_t TM_S = D, TM_DP = D + kBaTile;
+  uint8_t *sV = smem + 2 * Q_BYTES, *sK = sV + KV;      // K: one or two stages
+  const int NK = a.k_stages;
+  TcDqBars *B = reinterpret_cast<TcDqBars *>(sK + NK * KV);
+  uint32_t *bits = reinterpret_cast<uint32_t *>(sK + NK * KV + 128);
   const int tokens = a.tile_tokens;
   const int W = (a.nblk + 31) / 32;
   uint32_t *uni = bits + tokens * W;
@@ -526,16 +544,14 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
     tmem_relinquish();
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&B->k_full[i], 32);
       mbar_init(&B->k_empty[i], 1);
-      mbar_init(&B->v_full[i], 32);
-      mbar_init(&B->v_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&B->s_full[i], 1);
-      mbar_init(&B->ds_full[i], 128);
-    }
+    mbar_init(&B->v_full, 32);
+    mbar_init(&B->v_empty, 1);
+    mbar_init(&B->s_full, 1);
+    mbar_init(&B->ds_full, 256);
     mbar_init(&B->done, 1);
     mbar_init(&B->drain, 1);
     fence_mbar_init();
@@ -578,13 +594,8 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
     for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (c == 0) {
       const int64_t row = row_of(r);
-      row_delta[r] = s;
-      if (row >= 0) a.delta[row] = s;
+      if (row >= 0) a.delta[row] = s;               // read back below, by this CTA, after the barrier
     }
-  }
-  if (threadIdx.x < kTcRows) {
-    const int64_t row = row_of(threadIdx.x);
-    row_lse[threadIdx.x] = row >= 0 ? a.lse_in[row] * 1.4426950408889634f : 0.f;
   }
   __syncthreads();
   const uint32_t tmem = B->tmem;
@@ -595,13 +606,14 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
   if (warp >= 9) {
     // ---------------------------------------------------------------- loads: K, V
     const bool is_v = warp == 10;
-    uint64_t *full = is_v ? B->v_full : B->k_full, *empty = is_v ? B->v_empty : B->k_empty;
-    int st = 0, ph = 1;                             // the first round finds the stages empty
+    uint64_t *full = is_v ? &B->v_full : B->k_full, *empty = is_v ? &B->v_empty : B->k_empty;
+    const int stages = is_v ? 1 : NK;
+    int st = 0, ph = 1;
     for (int t = 0; t < steps && !a.fault; ++t) {
-      if (t >= NS && !tc_warp_wait(&empty[st], ph, ns)) break;
+      if (t >= stages && !tc_warp_wait(&empty[st], ph, ns)) break;
       tc_load_tile<D>(smem_u32(is_v ? sV : sK) + static_cast<uint32_t>(st) * KV, is_v ? vh : kh, un.key(t), len);
       cp_async_arrive(&full[st]);
-      if (++st == NS) {
+      if (++st == stages) {
         st = 0;
         ph ^= 1;
       }
@@ -616,40 +628,32 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
       const SmemDesc kd = make_desc_sw128(smem_u32(sK), 16, 1024);
       const SmemDesc vd = make_desc_sw128(smem_u32(sV), 16, 1024);
       const SmemDesc kn = make_desc_sw128(smem_u32(sK), kBaTile * 128, 1024);
-      int st = 0, ph = 0, done = 0, n_s = 0;        // stages of the next scores and dQ product; scores issued
-      auto issue_s = [&]() {                        // S and dP, into the buffers of the step's group
-        if (!tc_wait(&B->k_full[st], ph, ns) || !tc_wait(&B->v_full[st], ph, ns)) return false;
-        fence_proxy_async_smem();
+      int st = 0, ph = 0;                           // K's stage
+      for (int t = 0; t < steps; ++t) {
+        if (!tc_wait(&B->k_full[st], ph, ns) || !tc_wait(&B->v_full, t & 1, ns)) break;
+        const uint32_t off = static_cast<uint32_t>(st * KV) >> 4;
+        fence_proxy_async_smem();                   // cp.async writes -> tensor-core reads
         tc_fence_after();
-        const uint32_t off = static_cast<uint32_t>(st * KV) >> 4, buf = (n_s & 1) * kBaTile;
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + buf, qd, SmemDesc{kd.lo + off, kd.hi},
-                                                                IDESC_S, 0u);
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + buf, od, SmemDesc{vd.lo + off, vd.hi},
-                                                                IDESC_S, 0u);
-        mma_commit(&B->s_full[n_s & 1]);
-        mma_commit(&B->v_empty[st]);
-        ++n_s;
-        if (++st == NS) {
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S, qd, SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
+        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP, od, vd, IDESC_S, 0u);
+        mma_commit(&B->s_full);
+        mma_commit(&B->v_empty);
+        if (!tc_wait(&B->ds_full, t & 1, ns)) break;
+        tc_fence_after();
+        // 16 keys a step; a group's 32 columns hold its high parts, then the low ones
+#pragma unroll
+        for (int k = 0; k < 2 * kBaTile / 16; ++k) {
+          const int j = k & 3;
+          mma_bf16_ts(tmem, tmem + TM_S + 32 * (j >> 1) + 8 * (j & 1) + (k >= 4 ? 16 : 0),
+                      (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + ((j * 2048) >> 4)), IDESC_DQ,
+                      t > 0 || k > 0 ? 1u : 0u);
+        }
+        mma_commit(&B->k_empty[st]);
+        if (t == steps - 1) mma_commit(&B->done);
+        if (++st == NK) {
           st = 0;
           ph ^= 1;
         }
-        return true;
-      };
-      bool ok = steps == 0 || issue_s();
-      for (int t = 0; t < steps && ok; ++t) {
-        // the buffers of step t + 1 held dS(t - 1), whose product was issued before
-        if (t + 1 < steps && !issue_s()) break;
-        if (!tc_wait(&B->ds_full[t & 1], (t >> 1) & 1, ns)) break;
-        tc_fence_after();
-        const uint32_t off = static_cast<uint32_t>(done * KV) >> 4;
-#pragma unroll
-        for (int k = 0; k < 2 * kBaTile / 16; ++k)  // dS's high parts, then the low ones
-          mma_bf16_ts(tmem, tmem + TM_S + (t & 1) * kBaTile + 8 * k,
-                      (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + (((k & 3) * 2048) >> 4)), IDESC_DQ,
-                      t > 0 || k > 0 ? 1u : 0u);
-        mma_commit(&B->k_empty[done]);
-        if (t == steps - 1) mma_commit(&B->done);
-        if (++done == NS) done = 0;
       }
       mma_commit(&B->drain);
       mbar_wait(&B->drain, 0, 1000000000ull);
@@ -660,54 +664,53 @@ __global__ void __launch_bounds__(kTcDqThreads, 1) block_attn_dq_tc_kernel(const
     const int64_t row = row_of(r);
     const int tok = row >= 0 ? row_of.token(r) : 0;
     const int seen = row >= 0 ? query_seen(a, len, n0 + tok) : 0;
-    const float z = row_lse[r], delta = row_delta[r];
+    const float z = row >= 0 ? __ldg(a.lse_in + row) * 1.4426950408889634f : 0.f, delta = row >= 0 ? a.delta[row] : 0.f;
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_at = mine + TM_S + grp * kBaTile, p_at = mine + TM_DP + grp * kBaTile;
+    const uint32_t s_at = mine + TM_S + 32 * grp, p_at = mine + TM_DP + 32 * grp;
     bool ok = true;
-    for (int t = grp; t < steps; t += 2) {
-      const int key0 = un.key(t);
+    for (int t = 0; t < steps; ++t) {
+      const int key0 = un.key(t) + 32 * grp;
       const int end = row >= 0 && un.listed(tok, t) ? seen - key0 : 0;
-      if (!tc_warp_wait(&B->s_full[grp], (t >> 1) & 1, ns)) {
+      if (!tc_warp_wait(&B->s_full, t & 1, ns)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const bool any = __any_sync(0xffffffffu, end > 0), part = __any_sync(0xffffffffu, end > 0 && end < kBaTile);
-      float g[32], rest[32];
+      const bool any = __any_sync(0xffffffffu, end > 0), part = __any_sync(0xffffffffu, end > 0 && end < 32);
+      float g[32];                                  // high parts of 32 keys, low parts
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         if (any) {
-          float s[32], dp[32];
-          tmem_ld32_sync(s_at + 32 * h, s);
-          tmem_ld32_sync(p_at + 32 * h, dp);
+          float s[16], dp[16];
+          tmem_ld16_sync(s_at + 16 * h, s);
+          tmem_ld16_sync(p_at + 16 * h, dp);
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
+          for (int c = 0; c < 16; c += 2) {
             float d[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float p = ex2_approx(fmaf(s[c + e], a.scale_log2, -z));
               d[e] = p * (dp[c + e] - delta);
-              if (part) d[e] = 32 * h + c + e < end ? d[e] : 0.f;
+              if (part) d[e] = 16 * h + c + e < end ? d[e] : 0.f;
             }
             // dS as two bf16 parts (2^-16 relative): a row's dS add up to zero, so what the keys have in common
             // cancels in dQ, and rounding to one part would leave 2.5 times the error
             const uint32_t top = end > 0 ? pack_bf16x2(d[0], d[1]) : 0u;
-            g[16 * h + (c >> 1)] = __uint_as_float(top);
-            rest[16 * h + (c >> 1)] =
+            g[8 * h + (c >> 1)] = __uint_as_float(top);
+            g[16 + 8 * h + (c >> 1)] =
                 end > 0 ? __uint_as_float(pack_bf16x2(d[0] - __uint_as_float(top << 16),
                                                       d[1] - __uint_as_float(top & 0xFFFF0000u)))
                         : 0.f;
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < 16; ++c) g[16 * h + c] = rest[16 * h + c] = 0.f;
+          for (int c = 0; c < 8; ++c) g[8 * h + c] = g[16 + 8 * h + c] = 0.f;
         }
       }
       tmem_st32(s_at, g);
-      tmem_st32(s_at + 32, rest);
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&B->ds_full[grp]);
+      mbar_arrive(&B->ds_full);
     }
     if (grp == 0) {
       // ---- the accumulator: scaled, stored, rows that are not finite again

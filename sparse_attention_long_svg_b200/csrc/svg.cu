@@ -1030,7 +1030,7 @@ SelectArgs carve_select(void *ws, int BHk, int Nq, int nblk, int D, size_t *byte
   return a;
 }
 
-constexpr size_t kMaxSmem = 227 * 1024;
+constexpr size_t kMaxSmem = 227 * 1024, kHalfSmem = (228 * 1024 - 2 * 1024) / 2;   // one CTA per SM; two
 // Tokens of a 128-row tile: as many as fit with their bit sets (fewer only for
 // one or two heads to a key head and thousands of blocks).
 template <typename F>
@@ -1313,7 +1313,13 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
   const int sub = block / kBaTile;
   const int64_t tiles = static_cast<int64_t>(BHk) * nblk * sub;
   const int64_t listed = static_cast<int64_t>(BHk) * Nq * topk;
-  const int tokens = tile_tokens(BHq / BHk, [&](int t) { return D == 128 ? tc_dq_smem<128>(t, nblk) : tc_dq_smem<64>(t, nblk); });
+  auto dq_bytes = [&](int stages, int t) {
+    return D == 128 ? tc_dq_smem<128>(stages, t, nblk) : tc_dq_smem<64>(stages, t, nblk);
+  };
+  const int tokens = tile_tokens(BHq / BHk, [&](int t) { return dq_bytes(1, t); });
+  // A second stage of K where two CTAs still share an SM (D = 128: lists of up
+  // to a few hundred blocks).
+  const int k_stages = dq_bytes(2, tokens) <= kHalfSmem ? 2 : 1;
   const int64_t ctas = static_cast<int64_t>(BHk) * ((Nq + tokens - 1) / tokens);
   if (tiles >= (1ll << 31) - 1 || w.max_items >= (1ll << 31) - 1 || (listed + 255) / 256 >= (1ll << 31) ||
       ctas >= (1ll << 31))
@@ -1334,6 +1340,7 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
   a.part_kv = w.part_kv;
   a.item_tokens = w.item_tokens;
   a.tile_tokens = tokens;
+  a.k_stages = k_stages;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   st = cuda_status(cudaMemsetAsync(w.rev, 0, w.rev_bytes, s), "cudaMemsetAsync(block lists)");
   if (st != SVG_OK) return st;
@@ -1350,9 +1357,9 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
     return launch_status("block_attn gradient kernels");
   };
   if (D == 128)
-    return go(block_attn_dq_tc_kernel<128>, tc_dq_smem<128>(tokens, nblk), block_attn_dkv_tc_kernel<128>,
+    return go(block_attn_dq_tc_kernel<128>, dq_bytes(k_stages, tokens), block_attn_dkv_tc_kernel<128>,
               tc_dkv_smem<128>(w.item_tokens), block_attn_dkv_join_kernel<128>);
-  return go(block_attn_dq_tc_kernel<64>, tc_dq_smem<64>(tokens, nblk), block_attn_dkv_tc_kernel<64>,
+  return go(block_attn_dq_tc_kernel<64>, dq_bytes(k_stages, tokens), block_attn_dkv_tc_kernel<64>,
             tc_dkv_smem<64>(w.item_tokens), block_attn_dkv_join_kernel<64>);
 }
 
