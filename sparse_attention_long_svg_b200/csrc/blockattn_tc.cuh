@@ -71,17 +71,54 @@ __device__ __forceinline__ void tc_load_rows(uint32_t dst, const __nv_bfloat16 *
   }
 }
 
+// The issuing warp runs as a whole, with one elected lane behind a predicate of
+// each instruction: operands then are uniform registers.  Issued from a branch
+// that one lane takes, every descriptor word goes through a move to one, about
+// 80 clocks for each of these short products.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, SmemDesc a, uint32_t a_off, SmemDesc b, uint32_t b_off,
+                                          uint32_t idesc, uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 ad, bd;\n\t"
+      "mov.b64 ad, {%1, %2};\n\tmov.b64 bd, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 e, %7, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t}" ::"r"(d),
+      "r"(a.lo + a_off), "r"(a.hi), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+// A from TMEM (lane = row, two bf16 per column).
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, SmemDesc b, uint32_t b_off, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 bd;\n\t"
+      "mov.b64 bd, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b.lo + b_off), "r"(b.hi), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t *bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
+}
+// K16 steps into one accumulator: step k lies (k / 4) * X_HALF + (k % 4) * X_K bytes behind the operand's start.
+template <int STEPS, uint32_t A_HALF, uint32_t A_K, uint32_t B_HALF, uint32_t B_K>
+__device__ __forceinline__ void tc_chain(uint32_t d, SmemDesc a, SmemDesc b, uint32_t idesc, uint32_t accumulate_first,
+                                         uint32_t elected) {
+#pragma unroll
+  for (int k = 0; k < STEPS; ++k)
+    tc_mma_ss(d, a, ((k >> 2) * A_HALF + (k & 3) * A_K) >> 4, b, ((k >> 2) * B_HALF + (k & 3) * B_K) >> 4, idesc,
+              k > 0 ? 1u : accumulate_first, elected);
+}
+
 struct TcBars {                       // at most 192 bytes
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], done, last, drain;
   uint32_t tmem;
   int count;
 };
 
-__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
-  if (mbar_wait(bar, parity, ns)) return true;
-  record_error(SVG_ERR_TIMEOUT, SVG_SITE_BLOCK_ATTN);
-  return false;
-}
 __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
   const bool ok = mbar_wait(bar, parity, ns);
   if (!ok && lane_id() == 0) record_error(SVG_ERR_TIMEOUT, SVG_SITE_BLOCK_ATTN);
@@ -256,21 +293,22 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
     cp_async_wait<0>();
   } else if (warp == 4) {
     // ---------------------------------------------------------------- matrix products
-    if (lane == 0) {
+    {
+      const uint32_t el = elect_one();
       const SmemDesc qd = make_desc_sw128(smem_u32(smem), 16, 1024);
       const SmemDesc kd = make_desc_sw128(smem_u32(sKV), 16, 1024);
       const SmemDesc vd = make_desc_sw128(smem_u32(sKV) + KV, kBaTile * 128, 1024);
       int n_s = 0;                                  // score products issued
       auto issue_s = [&]() {
         const int st = n_s & 1;
-        if (!tc_wait(&B->k_full[st], (n_s >> 1) & 1, ns)) return false;
+        if (!tc_warp_wait(&B->k_full[st], (n_s >> 1) & 1, ns)) return false;
         fence_proxy_async_smem();                   // cp.async writes -> tensor-core reads
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, qd,
-                                                                SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
-        mma_commit(&B->s_full[st]);
-        mma_commit(&B->k_empty[st]);
+        tc_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, qd,
+                                                                SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u, el);
+        tc_commit(&B->s_full[st], el);
+        tc_commit(&B->k_empty[st], el);
         ++n_s;
         return true;
       };
@@ -279,20 +317,19 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
         const int st = t & 1;
         // its score buffer held P(t-1), whose product was issued before
         if (t + 1 < steps && !issue_s()) break;
-        if (!tc_wait(&B->v_full[st], (t >> 1) & 1, ns) || !tc_wait(&B->p_full[st], (t >> 1) & 1, ns)) break;
+        if (!tc_warp_wait(&B->v_full[st], (t >> 1) & 1, ns) || !tc_warp_wait(&B->p_full[st], (t >> 1) & 1, ns)) break;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * KV) >> 4;
 #pragma unroll
         for (int k = 0; k < kBaTile / 16; ++k)
-          mma_bf16_ts(tmem, tmem + TM_S + st * kBaTile + 8 * k,
-                      (static_cast<uint64_t>(vd.hi) << 32) | (vd.lo + off + ((k * 2048) >> 4)), IDESC_PV,
-                      t > 0 || k > 0 ? 1u : 0u);
-        mma_commit(&B->v_empty[st]);
-        mma_commit(&B->done);
-        if (t == steps - 1) mma_commit(&B->last);
+          tc_mma_ts(tmem, tmem + TM_S + st * kBaTile + 8 * k, vd, off + ((k * 2048) >> 4), IDESC_PV,
+                    t > 0 || k > 0 ? 1u : 0u, el);
+        tc_commit(&B->v_empty[st], el);
+        tc_commit(&B->done, el);
+        if (t == steps - 1) tc_commit(&B->last, el);
       }
-      mma_commit(&B->drain);                        // all retired before TMEM is released
+      tc_commit(&B->drain, el);                        // all retired before TMEM is released
       mbar_wait(&B->drain, 0, 1000000000ull);
     }
   } else {
@@ -622,7 +659,8 @@ __global__ void __launch_bounds__(kTcDqThreads, 2) block_attn_dq_tc_kernel(const
     cp_async_wait<0>();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- matrix products
-    if (lane == 0) {
+    {
+      const uint32_t el = elect_one();
       const SmemDesc qd = make_desc_sw128(smem_u32(smem), 16, 1024);
       const SmemDesc od = make_desc_sw128(smem_u32(smem) + Q_BYTES, 16, 1024);
       const SmemDesc kd = make_desc_sw128(smem_u32(sK), 16, 1024);
@@ -630,32 +668,32 @@ __global__ void __launch_bounds__(kTcDqThreads, 2) block_attn_dq_tc_kernel(const
       const SmemDesc kn = make_desc_sw128(smem_u32(sK), kBaTile * 128, 1024);
       int st = 0, ph = 0;                           // K's stage
       for (int t = 0; t < steps; ++t) {
-        if (!tc_wait(&B->k_full[st], ph, ns) || !tc_wait(&B->v_full, t & 1, ns)) break;
+        if (!tc_warp_wait(&B->k_full[st], ph, ns) || !tc_warp_wait(&B->v_full, t & 1, ns)) break;
         const uint32_t off = static_cast<uint32_t>(st * KV) >> 4;
         fence_proxy_async_smem();                   // cp.async writes -> tensor-core reads
         tc_fence_after();
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S, qd, SmemDesc{kd.lo + off, kd.hi}, IDESC_S, 0u);
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP, od, vd, IDESC_S, 0u);
-        mma_commit(&B->s_full);
-        mma_commit(&B->v_empty);
-        if (!tc_wait(&B->ds_full, t & 1, ns)) break;
+        tc_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S, qd, SmemDesc{kd.lo + off, kd.hi}, IDESC_S,
+                                                               0u, el);
+        tc_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP, od, vd, IDESC_S, 0u, el);
+        tc_commit(&B->s_full, el);
+        tc_commit(&B->v_empty, el);
+        if (!tc_warp_wait(&B->ds_full, t & 1, ns)) break;
         tc_fence_after();
         // 16 keys a step; a group's 32 columns hold its high parts, then the low ones
 #pragma unroll
         for (int k = 0; k < 2 * kBaTile / 16; ++k) {
           const int j = k & 3;
-          mma_bf16_ts(tmem, tmem + TM_S + 32 * (j >> 1) + 8 * (j & 1) + (k >= 4 ? 16 : 0),
-                      (static_cast<uint64_t>(kn.hi) << 32) | (kn.lo + off + ((j * 2048) >> 4)), IDESC_DQ,
-                      t > 0 || k > 0 ? 1u : 0u);
+          tc_mma_ts(tmem, tmem + TM_S + 32 * (j >> 1) + 8 * (j & 1) + (k >= 4 ? 16 : 0), kn, off + ((j * 2048) >> 4),
+                    IDESC_DQ, t > 0 || k > 0 ? 1u : 0u, el);
         }
-        mma_commit(&B->k_empty[st]);
-        if (t == steps - 1) mma_commit(&B->done);
+        tc_commit(&B->k_empty[st], el);
+        if (t == steps - 1) tc_commit(&B->done, el);
         if (++st == NK) {
           st = 0;
           ph ^= 1;
         }
       }
-      mma_commit(&B->drain);
+      tc_commit(&B->drain, el);
       mbar_wait(&B->drain, 0, 1000000000ull);
     }
   } else {
@@ -893,7 +931,8 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
     cp_async_wait<0>();
   } else if (warp == 8) {
     // ---------------------------------------------------------------- matrix products
-    if (lane == 0) {
+    {
+      const uint32_t el = elect_one();
       const SmemDesc od = make_desc_sw128(smem_u32(sQ), 16, 1024), qd = make_desc_sw128(smem_u32(sQ) + QT, 16, 1024);
       const SmemDesc kd = make_desc_sw128(smem_u32(sK), 16, 1024), vd = make_desc_sw128(smem_u32(sV), 16, 1024);
       // transposed operands: 64 channels (keys) of all rows, then the next 64
@@ -903,15 +942,15 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
       int n_s = 0;                                  // steps whose scores are issued
       auto issue_s = [&]() {
         const int st = n_s & 1;
-        if (!tc_wait(&B->q_full[st], (n_s >> 1) & 1, ns)) return false;
+        if (!tc_warp_wait(&B->q_full[st], (n_s >> 1) & 1, ns)) return false;
         fence_proxy_async_smem();
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, SmemDesc{qd.lo + off, qd.hi},
-                                                                kd, IDESC_S, 0u);
-        mma_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + st * kBaTile,
-                                                                SmemDesc{od.lo + off, od.hi}, vd, IDESC_S, 0u);
-        mma_commit(&B->s_full[st]);
+        tc_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_S + st * kBaTile, SmemDesc{qd.lo + off, qd.hi},
+                                                                kd, IDESC_S, 0u, el);
+        tc_chain<D / 16, kTcRows * 128, 32, kBaTile * 128, 32>(tmem + TM_DP + st * kBaTile,
+                                                                SmemDesc{od.lo + off, od.hi}, vd, IDESC_S, 0u, el);
+        tc_commit(&B->s_full[st], el);
         ++n_s;
         return true;
       };
@@ -921,22 +960,22 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
         // was announced), unless its rows are still on their way: step t's
         // products, which free a stage, must not wait for them.
         if (n_s == t && !issue_s()) break;
-        if (t + 1 < steps && mbar_test(&B->q_full[st ^ 1], ((t + 1) >> 1) & 1) && !issue_s()) break;
-        if (!tc_wait(&B->p_full, t & 1, ns)) break;
+        if (t + 1 < steps && __any_sync(0xffffffffu, mbar_test(&B->q_full[st ^ 1], ((t + 1) >> 1) & 1)) && !issue_s()) break;
+        if (!tc_warp_wait(&B->p_full, t & 1, ns)) break;
         tc_fence_after();
         const uint32_t off = static_cast<uint32_t>(st * 2 * QT) >> 4;
         const uint32_t more = t > 0 ? 1u : 0u;
         // K steps of 16 rows = 2048 bytes in both operands
-        mma_chain<kTcRows / 16, 4 * 2048, 2048, 4 * 2048, 2048>(tmem + TM_DV, SmemDesc{ot.lo + off, ot.hi}, pd, IDESC_G,
-                                                                more);
+        tc_chain<kTcRows / 16, 4 * 2048, 2048, 4 * 2048, 2048>(tmem + TM_DV, SmemDesc{ot.lo + off, ot.hi}, pd, IDESC_G,
+                                                                more, el);
         if (D == 128)
-          mma_chain<kTcRows / 16, 4 * 2048, 2048, 4 * 2048, 2048>(tmem + TM_DK, SmemDesc{qt.lo + off, qt.hi}, gd,
-                                                                  IDESC_G, more);
-        mma_commit(&B->q_empty[st]);
-        mma_commit(&B->p_free);
-        if (t == steps - 1) mma_commit(&B->done);
+          tc_chain<kTcRows / 16, 4 * 2048, 2048, 4 * 2048, 2048>(tmem + TM_DK, SmemDesc{qt.lo + off, qt.hi}, gd,
+                                                                  IDESC_G, more, el);
+        tc_commit(&B->q_empty[st], el);
+        tc_commit(&B->p_free, el);
+        if (t == steps - 1) tc_commit(&B->done, el);
       }
-      mma_commit(&B->drain);
+      tc_commit(&B->drain, el);
       mbar_wait(&B->drain, 0, 1000000000ull);
     }
   } else {
