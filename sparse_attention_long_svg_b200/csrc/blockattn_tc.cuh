@@ -217,7 +217,10 @@ __device__ __noinline__ void row_again(const TcUnion &un, const __nv_bfloat16 *q
 //   S(t+1) is issued before P(t) V, so the tensor cores run while the softmax
 //   of the other buffer (or of the SM's other CTA) does.
 // The reference maximum of a row is raised only when a score exceeds it by 2^8;
-// then the accumulator in TMEM is rescaled.
+// then the accumulator in TMEM is rescaled.  A step moves 96 KB through shared
+// memory (the short products read their operands from there), 770 of the about
+// 900 clocks it takes per SM: 500 us for 2 x 8,190 tokens, 40 / 8 heads, 16 blocks
+// (545 TFLOP/s of listed work), 1,190 us for 8 x 32,760 tokens, 32 blocks.
 template <int D>
 __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const BlockAttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -537,7 +540,7 @@ __device__ __forceinline__ void tmem_ld16_sync(uint32_t taddr, float (&v)[16]) {
 // forward kernel.  A step is a chain (K, V -> S, dP -> dS -> dQ), and a list is
 // short beside a CTA's start-up, so everything is held once and two CTAs share
 // an SM: one's chain and start-up fill the other's gaps (one CTA with three
-// stages and two score buffers took 650 us where this takes 460: 8,190 tokens,
+// stages and two score buffers took 650 us where this takes 470: 8,190 tokens,
 // 40 / 8 heads, 16 blocks).  Warps 0-7: two groups, 32 keys of a step each (a
 // TMEM lane belongs to a thread of each); a group's dS replaces its own scores
 // there, as the A operand of the product with K; warp 8 issues, 9 and 10 load.
@@ -804,6 +807,10 @@ __global__ void __launch_bounds__(kTcDqThreads, 2) block_attn_dq_tc_kernel(const
 // D = 64 would leave half of the 128 accumulator lanes empty, so there one
 // product [dO | Q]^T [P | dS] makes both (its other two quarters are not read).
 // Warps 0-7: two groups, 32 keys each; warp 8: matrix products; warps 9-12: loads.
+// A step moves 288 KB through shared memory (operands 192, gathered rows 64, P and
+// dS 32), 2,300 of the 3,200 clocks it takes: 650 us for 8,190 tokens, 40 / 8 heads,
+// 16 blocks.  Sums of one item stay in TMEM; items of 4,096 rows keep the fp32
+// slots of a tile with several at a tenth of the time.
 constexpr int kTcDkvThreads = 13 * 32;
 
 struct TcDkvBars {                     // at most 256 bytes

