@@ -406,8 +406,9 @@ svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, 
 /* o [BHq, Nq, D] bf16, lse [BHq, Nq] fp32 (natural log, NULL to skip).  Lists
  * may be in any order; ids outside [0, nblk) are passed over and an id given
  * twice counts once.  A query without a visible key gets zeros and lse = -inf.
- * scale <= 0 selects 1/sqrt(D).  Blocks that a query does not list and rows
- * beyond kv_len do not reach it, whatever they hold. */
+ * scale <= 0 selects 1/sqrt(D).  Keys that a query does not see (blocks it does
+ * not list, later tokens, rows beyond kv_len) do not reach it, whatever they
+ * hold. */
 size_t svg_block_attn_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block);
 svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, int BHk, int B, int Nq, int Nk, int D,
                           const int32_t *sel, int topk, int block, int causal, float scale, const int32_t *kv_len,

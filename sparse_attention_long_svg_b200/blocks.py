@@ -84,6 +84,8 @@ def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Te
 def _scratch(workspace, nbytes: int, device):
     """(workspace or None, its size): nothing is allocated where a call needs none."""
     if workspace is not None:
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
         return workspace, workspace.numel() * workspace.element_size()
     if nbytes == 0:
         return None, 0

@@ -178,6 +178,84 @@ __host__ __device__ inline size_t block_attn_smem(int rows, int tokens, int nblk
   return static_cast<size_t>(rows) * D * 2 + 16 + mark_bytes(tokens, nblk);
 }
 
+__device__ __forceinline__ float dot_rows(const __nv_bfloat16 *a, const __nv_bfloat16 *b, int D) {
+  float s = 0.f;
+  for (int c = 0; c < D; c += 8) {
+    float x[8], y[8];
+    unpack8(*reinterpret_cast<const uint4 *>(a + c), x);
+    unpack8(*reinterpret_cast<const uint4 *>(b + c), y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += x[e] * y[e];
+  }
+  return s;
+}
+
+// What the CTA's rows share, for the row that is computed again: tiles [u0, u1)
+// of the union (key(u)), the row's bit set.
+struct BaUnion {
+  const uint16_t *list;
+  const uint32_t *bits;
+  int u0, u1, keys, shift, tokens;     // a block has 2^shift tiles of `keys` keys
+  __device__ __forceinline__ int block_of(int u) const { return list[u >> shift]; }
+  __device__ __forceinline__ int key(int u) const {
+    return ((block_of(u) << shift) + (u & ((1 << shift) - 1))) * keys;
+  }
+  __device__ __forceinline__ bool listed(int tok, int u) const {
+    const int j = block_of(u);
+    return (bits[(j >> 5) * tokens + tok] >> (j & 31)) & 1u;
+  }
+};
+
+// One row by one warp, from its own keys alone: two passes over the scores.
+// Lane i ends with channels i * D/32 ... of the normalised output.
+template <int D>
+__device__ __noinline__ void row_again(const BaUnion &un, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
+                                       const __nv_bfloat16 *v, int tok, int seen, float sl2, float (&y)[D / 32],
+                                       float &lse2) {
+  constexpr int E = D / 32;
+  const int lane = lane_id();
+  float m = -INFINITY, l = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = 0.f;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int u = un.u0; u < un.u1; ++u) {
+      if (!un.listed(tok, u)) continue;
+      const int key0 = un.key(u), end = min(seen - key0, un.keys);
+      for (int j0 = 0; j0 < end; j0 += 32) {
+        const bool in = j0 + lane < end;
+        float s = -INFINITY;
+        if (in) s = dot_rows(q, k + static_cast<int64_t>(key0 + j0 + lane) * D, D) * sl2;
+        if (pass == 0) {
+          m = fmaxf(m, s);
+          nan = nan || s != s;
+          continue;
+        }
+        const float p = in ? ex2_approx(s - m) : 0.f;
+        l += p;
+        for (int j = 0; j < min(32, end - j0); ++j) {
+          const float pj = __shfl_sync(0xffffffffu, p, j);
+          const __nv_bfloat16 *vr = v + static_cast<int64_t>(key0 + j0 + j) * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) y[e] += pj * __bfloat162float(vr[e]);
+        }
+      }
+    }
+    if (pass == 0) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (__any_sync(0xffffffffu, nan)) m = __int_as_float(0x7FC00000);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  // scores of minus infinity only: as without keys
+  const float inv = m == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < E; ++e) y[e] = m == -INFINITY ? 0.f : y[e] * inv;
+  lse2 = m == -INFINITY ? -INFINITY : m + log2f(l);
+}
+
 // Few queries (at most floor(16/G), single tokens among them): all warps hold
 // the same 16 rows and take every fourth tile of 32 keys, each through its own
 // three buffers, so that 128 KB and more are always on their way (HBM bound:
@@ -349,6 +427,8 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_few_kernel(const Blo
   __syncthreads();
   float *so = reinterpret_cast<float *>(smem);
   float *sm = so + 4 * 16 * D, *sl = sm + 64;
+  int *bad = reinterpret_cast<int *>(sl + 64);
+  if (threadIdx.x < 16) bad[threadIdx.x] = 0;
   const int r0 = frag_row();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -386,6 +466,7 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_few_kernel(const Blo
     y0 *= inv;
     y1 *= inv;
     const float lse2 = none ? -INFINITY : m + log2f(l);
+    if (!none && !(fabsf(y0) < INFINITY && fabsf(y1) < INFINITY)) bad[r] = 1;
     if (a.splits > 1) {
       const int64_t pr = static_cast<int64_t>(blockIdx.y) * a.BHk * a.G * a.Nq + x.row;
       *reinterpret_cast<float2 *>(a.part_o + pr * D + c) = make_float2(y0, y1);
@@ -393,6 +474,37 @@ __global__ void __launch_bounds__(kBaThreads, 1) block_attn_few_kernel(const Blo
     } else {
       *reinterpret_cast<uint32_t *>(a.o + x.row * D + c) = pack_bf16(y0, y1);
       if (c == 0 && a.lse) a.lse[x.row] = lse2 * 0.69314718055994531f;
+    }
+  }
+  // Weights of zero do not stop an infinity or NaN: rows that are not finite
+  // again, from their own keys (a later token's key in the same tile).
+  __syncthreads();
+  BaUnion un;
+  un.list = list;
+  un.bits = bits;
+  un.u0 = u0;
+  un.u1 = u1;
+  un.keys = KEYS;
+  un.shift = a.block == 64 ? 1 : 2;
+  un.tokens = tokens;
+  for (int r = warp; r < 16; r += 4) {
+    if (!bad[r]) continue;
+    const BaRow x = ba_row(a, head, len, n0, 0, r);
+    float y[D / 32], z;
+    row_again<D>(un, a.q + x.row * D, kh, vh, x.tok, x.seen, a.scale_log2, y, z);
+    const int64_t pr = static_cast<int64_t>(blockIdx.y) * a.BHk * a.G * a.Nq + x.row;
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2) {
+      if (a.splits > 1)
+        *reinterpret_cast<float2 *>(a.part_o + pr * D + lane_id() * (D / 32) + e) = make_float2(y[e], y[e + 1]);
+      else
+        *reinterpret_cast<uint32_t *>(a.o + x.row * D + lane_id() * (D / 32) + e) = pack_bf16(y[e], y[e + 1]);
+    }
+    if (lane_id() == 0) {
+      if (a.splits > 1)
+        a.part_lse[pr] = z;
+      else if (a.lse)
+        a.lse[x.row] = z * 0.69314718055994531f;
     }
   }
 }

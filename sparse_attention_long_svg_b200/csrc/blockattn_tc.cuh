@@ -132,84 +132,6 @@ __host__ __device__ inline size_t tc_smem(int operands, int tokens, int nblk) {
   return static_cast<size_t>(operands) * kTcRows * D * 2 + 4ull * kBaTile * D * 2 + 192 + mark_bytes(tokens, nblk);
 }
 
-__device__ __forceinline__ float dot_rows(const __nv_bfloat16 *a, const __nv_bfloat16 *b, int D) {
-  float s = 0.f;
-  for (int c = 0; c < D; c += 8) {
-    float x[8], y[8];
-    unpack8(*reinterpret_cast<const uint4 *>(a + c), x);
-    unpack8(*reinterpret_cast<const uint4 *>(b + c), y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[e] * y[e];
-  }
-  return s;
-}
-
-// What the CTA's rows share, for the row that is computed again: tiles [u0, u1)
-// of the union (key(u)), the row's bit set.
-struct TcUnion {
-  const uint16_t *list;
-  const uint32_t *bits;
-  int u0, u1, shift, tokens;           // a block has 2^shift tiles of 64 keys
-  __device__ __forceinline__ int block_of(int u) const { return list[u >> shift]; }
-  __device__ __forceinline__ int key(int u) const {
-    return ((block_of(u) << shift) + (u & ((1 << shift) - 1))) * kBaTile;
-  }
-  __device__ __forceinline__ bool listed(int tok, int u) const {
-    const int j = block_of(u);
-    return (bits[(j >> 5) * tokens + tok] >> (j & 31)) & 1u;
-  }
-};
-
-// One row by one warp, from its own keys alone: two passes over the scores.
-// Lane i ends with channels i * D/32 ... of the normalised output.
-template <int D>
-__device__ __noinline__ void row_again(const TcUnion &un, const __nv_bfloat16 *q, const __nv_bfloat16 *k,
-                                       const __nv_bfloat16 *v, int tok, int seen, float sl2, float (&y)[D / 32],
-                                       float &lse2) {
-  constexpr int E = D / 32;
-  const int lane = lane_id();
-  float m = -INFINITY, l = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = 0.f;
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int u = un.u0; u < un.u1; ++u) {
-      if (!un.listed(tok, u)) continue;
-      const int key0 = un.key(u), end = min(seen - key0, kBaTile);
-      for (int j0 = 0; j0 < end; j0 += 32) {
-        const bool in = j0 + lane < end;
-        float s = -INFINITY;
-        if (in) s = dot_rows(q, k + static_cast<int64_t>(key0 + j0 + lane) * D, D) * sl2;
-        if (pass == 0) {
-          m = fmaxf(m, s);
-          nan = nan || s != s;
-          continue;
-        }
-        const float p = in ? ex2_approx(s - m) : 0.f;
-        l += p;
-        for (int j = 0; j < min(32, end - j0); ++j) {
-          const float pj = __shfl_sync(0xffffffffu, p, j);
-          const __nv_bfloat16 *vr = v + static_cast<int64_t>(key0 + j0 + j) * D + lane * E;
-#pragma unroll
-          for (int e = 0; e < E; ++e) y[e] += pj * __bfloat162float(vr[e]);
-        }
-      }
-    }
-    if (pass == 0) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (__any_sync(0xffffffffu, nan)) m = __int_as_float(0x7FC00000);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  // scores of minus infinity only: as without keys
-  const float inv = m == -INFINITY ? 0.f : 1.f / l;
-#pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = m == -INFINITY ? 0.f : y[e] * inv;
-  lse2 = m == -INFINITY ? -INFINITY : m + log2f(l);
-}
-
 // Warps 0-3: softmax (thread = row = TMEM lane); warp 4: its lane 0 issues the
 // matrix products; warp 5 loads K, warp 6 V (two stages each: a K tile is free
 // again before the weights of its scores are).  Two score buffers in TMEM; a row's
@@ -263,9 +185,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
   }
   tc_load_rows<D, kTcThreads>(smem_u32(smem), a.q, row_of);
   cp_async_commit();
-  TcUnion un;
+  BaUnion un;
   un.list = list;
   un.bits = bits;
+  un.keys = kBaTile;
   un.shift = a.block == kBaTile ? 0 : 1;
   un.tokens = tokens;
   tc_fence_before();
@@ -495,7 +418,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) block_attn_tc_kernel(const Bloc
 // ------------------------------------------------------------------ gradient
 // One row of dQ by one warp, from its own keys alone (see row_again).
 template <int D>
-__device__ __noinline__ void dq_row_again(const TcUnion &un, const __nv_bfloat16 *q, const __nv_bfloat16 *dout,
+__device__ __noinline__ void dq_row_again(const BaUnion &un, const __nv_bfloat16 *q, const __nv_bfloat16 *dout,
                                           const __nv_bfloat16 *k, const __nv_bfloat16 *v, int tok, int seen, float sl2,
                                           float lse2, float delta, float (&y)[D / 32]) {
   constexpr int E = D / 32;
@@ -504,7 +427,7 @@ __device__ __noinline__ void dq_row_again(const TcUnion &un, const __nv_bfloat16
   for (int e = 0; e < E; ++e) y[e] = 0.f;
   for (int u = un.u0; u < un.u1; ++u) {
     if (!un.listed(tok, u)) continue;
-    const int key0 = un.key(u), end = min(seen - key0, kBaTile);
+    const int key0 = un.key(u), end = min(seen - key0, un.keys);
     for (int j0 = 0; j0 < end; j0 += 32) {
       float ds = 0.f;
       if (j0 + lane < end) {
@@ -608,9 +531,10 @@ __global__ void __launch_bounds__(kTcDqThreads, 2) block_attn_dq_tc_kernel(const
     const int64_t row = i < kTcRows * (D / 8) ? row_of(i / (D / 8)) : -1;
     o_row[k] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.out + row * D + 8 * (i % (D / 8)))) : make_uint4(0, 0, 0, 0);
   }
-  TcUnion un;
+  BaUnion un;
   un.list = list;
   un.bits = bits;
+  un.keys = kBaTile;
   un.shift = a.block == kBaTile ? 0 : 1;
   un.tokens = tokens;
   un.u0 = 0;

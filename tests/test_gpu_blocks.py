@@ -479,6 +479,37 @@ def test_future_keys_that_are_not_finite_stay_in_the_future():
         assert a.isfinite().all() and (a - b).norm() <= 0.02 * b.norm()
 
 
+@pytest.mark.parametrize("Nk", [130, 4000])
+def test_a_token_that_is_not_finite_leaves_earlier_ones_alone(Nk):
+    """Three new tokens of which the last holds NaN and infinities: one matrix tile holds all three."""
+    Nq, D = 3, 64
+    q, k, v = tokens(89, 2, 4, 2, Nq, Nk, D)
+    sel = torch.arange(-(-Nk // 64), dtype=torch.int32, device="cuda").expand(4, Nq, -1).contiguous()
+    clean, lse = svg.block_attn(q, k, v, sel, 64, True, want_lse=True)
+    v[:, -1] = float("nan")
+    k[0, -1] = float("inf")
+    o, lse2 = svg.block_attn(q, k, v, sel, 64, True, want_lse=True)
+    assert (o[:, :2].float() - clean[:, :2].float()).abs().max() <= 2 * bo.HALF_BF16 * 4
+    assert (lse2[:, :2] - lse[:, :2]).abs().max() <= 1e-5 * (1 + lse.abs().max())
+    assert o[:, 2].isnan().any(-1).all()
+
+
+def test_gradient_without_keys():
+    """Q alone (cross attention prepares K elsewhere)."""
+    q, _, _, w_q, _ = rope_inputs(1, 9, 4, 1, 64, seed=130)
+    cos, sin = svg.rope_table((9,), 64)
+    qo, ko, vo = svg.qk_norm_rope(q, None, None, w_q, None, cos, sin)
+    assert ko is None and vo is None
+    dqo = bf(131, 4, 9, 64)
+    dq, dk, dv, dw_q, dw_k = svg.qk_norm_rope_backward(dqo, None, None, q, None, w_q, None, cos, sin)
+    assert dk is None and dv is None and dw_k is None
+    pos = np.arange(9)[None]
+    want, want_w, size, terms = bo.norm_rope_backward(f64(q), f64(w_q), f64(cos), f64(sin), 1e-6, True, pos,
+                                                      f64(dqo).reshape(1, 4, 9, 64))
+    within(dq, want, bo.HALF_BF16 * np.abs(want) + 300 * bo.HALF_F32 * size)
+    within(dw_q, want_w, 600 * bo.HALF_F32 * terms)
+
+
 def test_a_sequence_of_4096_blocks():
     """The longest list of blocks; its bit sets leave the gradient half a tile of tokens."""
     Hq, Nq, Nk, D = 2, 150, 262144, 128
