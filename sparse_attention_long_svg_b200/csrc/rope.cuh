@@ -12,8 +12,8 @@
 // thread and every access is 16 bytes.  A thread keeps its token's 8 cosines
 // and sines while it walks over a chunk of the token's heads.
 // Measured: forward 338 us for 32,760 tokens x 40 heads x D = 128 with V (2.03 GB,
-// 6.0 TB/s); gradient 46 us + 5 us (dw) for 10,002 tokens, 32 / 8 heads, D = 64
-// (175 MB, 3.4 TB/s: rows in 64-byte halves).
+// 6.0 TB/s); gradient 36 us + 5 us (dw) for 10,002 tokens, 32 / 8 heads, D = 64
+// (175 MB, 4.9 TB/s; 8 heads to a chunk and 96 registers: 43 us).
 #pragma once
 
 #include "common.cuh"
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
 constexpr int kRopeBackThreads = 128;
 
 template <int D, bool INTER>
-__global__ void __launch_bounds__(kRopeBackThreads, 5) qk_norm_rope_backward_kernel(const RopeArgs p) {
+__global__ void __launch_bounds__(kRopeBackThreads, 4) qk_norm_rope_backward_kernel(const RopeArgs p) {
   constexpr int GT = D / 16, GROUPS = kRopeBackThreads / GT;
   __shared__ float sums[GROUPS][D];
   const int c = threadIdx.x % GT, grp = threadIdx.x / GT;
