@@ -211,6 +211,15 @@ __device__ __forceinline__ float norm_part(float sum, const float (&v)[E]) {
   return none ? 0.f : sum < kNormFloor ? kNormFloor : sum;
 }
 
+// Largest error of approximate scores, `rel` times the norms' product.  Where
+// that product nears fp32's range (or is not a number), scores or their partial
+// sums may be infinite or NaN: the bound is infinite, and all are compared
+// exactly.
+__device__ __forceinline__ float score_bound(float rel, float q_norm, float mean_norm) {
+  const float size = q_norm * mean_norm;
+  return size <= 3.0e38f ? rel * size : INFINITY;
+}
+
 // Where an approximate score stands against the last place's, t: above (in),
 // near (to be compared exactly), else out.  Written so that an infinite bound
 // or a NaN makes everything near.
@@ -254,7 +263,7 @@ __device__ __noinline__ uint32_t rank_near(const SelectArgs &a, const int *near,
 // places without one are NaN, which no comparison takes) and finds the last
 // place's score from the lanes' largest ones (up to 32 places), or by bisection.
 // Returns false, with nothing written, for rows that are flat (more than 32
-// near the border) or hold infinities.
+// near the border) or whose scores have no finite bound.
 template <int D, int VPL>
 __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, int *near_list, float bound, int head,
                                            int n, const SelectRange &r) {
@@ -267,6 +276,8 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
     return true;
   }
   const int need = a.topk - r.num_forced();
+  // (with an infinite bound the borders t +- 2 bound could be NaN below)
+  if (need == 0 || !(bound < INFINITY)) return false;
   const float none = __int_as_float(0x7FFFFFFF);
   float f[VPL], mine = -INFINITY;
 #pragma unroll
@@ -281,7 +292,6 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
     f[i] = j < r.s1 || (j >= r.l0 && j < r.l1) || j >= r.may ? none : fmaxf(f[i], -INFINITY);
     mine = fmaxf(mine, f[i]);
   }
-  if (need == 0) return false;
   // the lanes' largest scores in descending order
   float best = mine;
 #pragma unroll
@@ -358,7 +368,7 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
   const int sure = both & 0xFFFF, nears = both >> 16;
   uint32_t stay = all;
   if (nears > need - sure) {
-    if (nears > 32 || !(bound < INFINITY)) return false;
+    if (nears > 32) return false;
     int at = 0;
 #pragma unroll
     for (int w = 0; w < WORDS; ++w) {
@@ -685,8 +695,7 @@ __global__ void __launch_bounds__(kSelThreads, 3) block_select_score_kernel(cons
       __syncthreads();
     }
     if (threadIdx.x < kSelTile) {
-      const float bound = kSelSplitError * qn[threadIdx.x] * sqrtf(norm);
-      a.bounds[blockIdx.x * kSelTile + threadIdx.x] = bound <= 3.4e38f ? bound : INFINITY;
+      a.bounds[blockIdx.x * kSelTile + threadIdx.x] = score_bound(kSelSplitError, qn[threadIdx.x], sqrtf(norm));
     }
   }
 }
@@ -831,8 +840,7 @@ __global__ void __launch_bounds__(kSelDecodeThreads, 1) block_select_decode_kern
   biggest = __reduce_max_sync(0xffffffffu, biggest);
   if (lane_id() == 0) atomicMax(&mn, biggest);
   __syncthreads();
-  float bound = kSelDotError * sqrtf(qa) * sqrtf(__uint_as_float(mn));
-  if (!(bound <= 3.4e38f)) bound = INFINITY;
+  const float bound = score_bound(kSelDotError, sqrtf(qa), sqrtf(__uint_as_float(mn)));
 
   // block i * 512 + thread, place i
   const int forced = r.num_forced();
