@@ -98,6 +98,16 @@ __device__ __forceinline__ void rope_angles(const RopeArgs &p, int64_t pos, int 
   sn[4] = s1.x; sn[5] = s1.y; sn[6] = s1.z; sn[7] = s1.w;
 }
 
+// Whether a token's row of tensor t counts: a position that is not negative
+// (padding), inside the table (for V as well: a cache row is whole or left
+// alone) and, as `row`, inside the tensor's buffer.  Others than padding are recorded.
+__device__ __forceinline__ bool rope_counts(const RopeArgs &p, int t, int64_t pos, int64_t row) {
+  if (pos < 0) return false;
+  if ((p.cos == nullptr || pos < p.P) && row < p.cap[t]) return true;
+  record_error(SVG_ERR_DEVICE_CHECK, SVG_SITE_ROPE_RANGE);
+  return false;
+}
+
 template <int D>
 __device__ __forceinline__ void rope_weights(const float *w, int c, float (&wa)[8], float (&wb)[8]) {
 #pragma unroll
@@ -139,12 +149,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
   const int t = live ? rope_chunk(p, chunk, h0, h1) : 0;
   const int64_t pos = static_cast<int64_t>(p.start ? p.start[b] : 0) + n;
   const int64_t row = t == 0 ? n : pos;
-  // negative positions are padding; others must lie inside the table and the buffer
-  bool ok = live && pos >= 0;
-  if (ok && ((t != 2 && p.cos && pos >= p.P) || row >= p.cap[t])) {
-    record_error(SVG_ERR_DEVICE_CHECK, SVG_SITE_ROPE_RANGE);
-    ok = false;
-  }
+  const bool ok = live && rope_counts(p, t, pos, row);
   float cs[8], sn[8], wa[8], wb[8];
   const bool turn = ok && t != 2 && p.cos != nullptr;
   if (turn) rope_angles<D, INTER>(p, pos, c, cs, sn);
@@ -222,11 +227,7 @@ __global__ void __launch_bounds__(kRopeBackThreads, 4) qk_norm_rope_backward_ker
     const int b = live ? static_cast<int>(tok / p.N) : 0, n = live ? static_cast<int>(tok % p.N) : 0;
     const int64_t pos = static_cast<int64_t>(p.start ? p.start[b] : 0) + n;
     const int64_t row = t == 0 ? n : pos;
-    bool ok = live && pos >= 0;
-    if (ok && ((t != 2 && p.cos && pos >= p.P) || row >= p.cap[t])) {
-      record_error(SVG_ERR_DEVICE_CHECK, SVG_SITE_ROPE_RANGE);
-      ok = false;
-    }
+    const bool ok = live && rope_counts(p, t, pos, row);
     const __nv_bfloat16 *x = t == 2 ? nullptr : p.x[t] + b * p.xb[t] + n * p.xn[t] + 8 * c;
     // rows that do not count are read all the same, at a row that exists
     const int64_t from = ok ? row : 0;

@@ -33,3 +33,58 @@ def test_selection_of_scores_beyond_fp32(Nq, nblk, topk):
     svg.block_select(q, mean, 64, topk, Nk, 1, 1, True, sel=sel)
     want = bo.select_blocks(f64(q), f64(mean), 64, topk, 1, 1, True, [Nk] * 4)
     assert np.array_equal(sel.cpu().numpy(), want), np.argwhere(sel.cpu().numpy() != want)[:5]
+
+
+# ----------------------------------------------------------------------- norm and rotation
+def test_tokens_beyond_the_table_leave_every_cache_row_alone():
+    """P <= position < cap: as for padding, Q's row is zero and neither K nor V is stored; the gradient is zero."""
+    B, N, H, D, cap, P = 2, 5, 3, 64, 20, 8
+    q, k, v, w_q, w_k = rope_inputs(B, N, H, H, D, seed=210)
+    cos, sin = svg.rope_table((P,), D)
+    start = i32(5, 1)                                # positions 5 .. 9 and 1 .. 5
+    ko, vo = bf(213, B * H, cap, D), bf(214, B * H, cap, D)
+    old_k, old_v = ko.clone(), vo.clone()
+    qo, _, _ = svg.qk_norm_rope(q, k, v, w_q, w_k, cos, sin, start=start, k_out=ko, v_out=vo)
+    assert svg.get_error_detail()[:2] == (6, "rotation range")
+    pos = np.array([[5, 6, 7, -1, -1], [1, 2, 3, 4, 5]])          # beyond the table: as padding
+    check_rows(qo, q, w_q, cos, sin, 1e-6, True, pos, "q")
+    for b in range(B):
+        rows = pos[b][pos[b] >= 0].tolist()
+        kept = [r for r in range(cap) if r not in rows]
+        heads = slice(b * H, (b + 1) * H)
+        assert torch.equal(vo[heads][:, rows], v[b, :len(rows)].transpose(0, 1))
+        assert torch.equal(vo[heads][:, kept], old_v[heads][:, kept])
+        assert torch.equal(ko[heads][:, kept], old_k[heads][:, kept])
+        assert (ko[heads][:, rows] != old_k[heads][:, rows]).any(-1).all()
+    dqo, dko, dvo = bf(215, B * H, N, D), bf(216, B * H, cap, D), bf(217, B * H, cap, D)
+    dq, dk, dv, dw_q, dw_k = svg.qk_norm_rope_backward(dqo, dko, dvo, q, k, w_q, w_k, cos, sin, start=start)
+    assert svg.get_error_detail()[:2] == (6, "rotation range")
+    for x in (dq, dk, dv):
+        assert not x[0, 3:].any() and x[0, :3].any(-1).all() and x[1].any(-1).all()
+    want, want_w, size, terms = bo.norm_rope_backward(f64(q), f64(w_q), f64(cos), f64(sin), 1e-6, True, pos,
+                                                      f64(dqo).reshape(B, H, N, D))
+    within(dq, want, bo.HALF_BF16 * np.abs(want) + 300 * bo.HALF_F32 * size, "dq")
+    within(dw_q, want_w, 600 * bo.HALF_F32 * terms, "dw_q")
+
+
+def test_tokens_beyond_the_buffer_but_in_the_table():
+    """cap <= position < P: Q has its row (and its gradient), K and V have none to go to."""
+    N, H, D, cap = 4, 2, 64, 6
+    q, k, v, w_q, w_k = rope_inputs(1, N, H, H, D, seed=220)
+    cos, sin = svg.rope_table((12,), D)
+    ko, vo = bf(223, H, cap, D), bf(224, H, cap, D)
+    old_k, old_v = ko.clone(), vo.clone()
+    qo, _, _ = svg.qk_norm_rope(q, k, v, w_q, w_k, cos, sin, start=i32(4), k_out=ko, v_out=vo)    # 4 .. 7
+    assert svg.get_error_detail()[:2] == (6, "rotation range")
+    pos = np.array([[4, 5, 6, 7]])
+    check_rows(qo, q, w_q, cos, sin, 1e-6, True, pos, "q")
+    assert torch.equal(ko[:, :4], old_k[:, :4]) and torch.equal(vo[:, :4], old_v[:, :4])
+    assert torch.equal(vo[:, 4:], v[0, :2].transpose(0, 1))
+    dqo, dko, dvo = bf(225, H, N, D), bf(226, H, cap, D), bf(227, H, cap, D)
+    dq, dk, dv, dw_q, _ = svg.qk_norm_rope_backward(dqo, dko, dvo, q, k, w_q, w_k, cos, sin, start=i32(4))
+    assert svg.get_error() == 6
+    want, want_w, size, terms = bo.norm_rope_backward(f64(q), f64(w_q), f64(cos), f64(sin), 1e-6, True, pos,
+                                                      f64(dqo).reshape(1, H, N, D))
+    within(dq, want, bo.HALF_BF16 * np.abs(want) + 300 * bo.HALF_F32 * size, "dq")
+    within(dw_q, want_w, 600 * bo.HALF_F32 * terms, "dw_q")
+    assert not dk[0, 2:].any() and not dv[0, 2:].any() and dk[0, :2].any(-1).all()
