@@ -408,7 +408,8 @@ svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, 
 
 /* o [BHq, Nq, D] bf16, lse [BHq, Nq] fp32 (natural log, NULL to skip).  Lists
  * may be in any order; ids outside [0, nblk) are passed over and an id given
- * twice counts once.  A query without a visible key gets zeros and lse = -inf.
+ * twice counts once.  A query without a visible key, or whose scores (fp32) are
+ * all -inf, gets zeros and lse = -inf.
  * scale <= 0 selects 1/sqrt(D).  Keys that a query does not see (blocks it does
  * not list, later tokens, rows beyond kv_len) do not reach it, whatever they
  * hold. */
@@ -419,7 +420,10 @@ svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, 
 
 /* dq [BHq, Nq, D], dk, dv [BHk, Nk, D] bf16 from dout, the forward call's
  * inputs and its o and lse.  Every element is written (zeros where nothing
- * was listed); sums run in a fixed order. */
+ * was listed); sums run in a fixed order.  A query with lse = -inf (no visible
+ * key, or no score above -inf) has no part in it.  A query whose q or dout is
+ * not finite reaches dk and dv of every key of a 64-key tile of which it sees
+ * any. */
 size_t svg_block_attn_backward_workspace_size(int BHq, int BHk, int Nq, int Nk, int D, int topk, int block);
 svg_status svg_block_attn_backward(const void *dout, const void *q, const void *k, const void *v, const void *o,
                                    const float *lse, int BHq, int BHk, int B, int Nq, int Nk, int D,

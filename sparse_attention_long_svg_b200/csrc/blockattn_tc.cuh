@@ -628,8 +628,9 @@ __global__ void __launch_bounds__(kTcDqThreads, 2) block_attn_dq_tc_kernel(const
     const int grp = warp >> 2, r = (warp & 3) * 32 + lane;
     const int64_t row = row_of(r);
     const int tok = row >= 0 ? row_of.token(r) : 0;
-    const int seen = row >= 0 ? query_seen(a, len, n0 + tok) : 0;
     const float z = row >= 0 ? __ldg(a.lse_in + row) * 1.4426950408889634f : 0.f, delta = row >= 0 ? a.delta[row] : 0.f;
+    // a row without a finite score (lse = -inf) is constant: it sees nothing here
+    const int seen = row >= 0 && z != -INFINITY ? query_seen(a, len, n0 + tok) : 0;
     const uint32_t mine = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_at = mine + TM_S + 32 * grp, p_at = mine + TM_DP + 32 * grp;
     bool ok = true;
@@ -924,7 +925,7 @@ __global__ void __launch_bounds__(kTcDkvThreads, 1) block_attn_dkv_tc_kernel(con
         const int64_t at = source(i, n);
         z_next = __ldg(a.lse_in + at);
         d_next = a.delta[at];
-        seen_next = query_seen(a, len, n);
+        seen_next = z_next != -INFINITY ? query_seen(a, len, n) : 0;   // as in the dQ kernel
       }
     };
     row_values(0);

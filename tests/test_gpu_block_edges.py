@@ -88,3 +88,31 @@ def test_tokens_beyond_the_buffer_but_in_the_table():
     within(dq, want, bo.HALF_BF16 * np.abs(want) + 300 * bo.HALF_F32 * size, "dq")
     within(dw_q, want_w, 600 * bo.HALF_F32 * terms, "dw_q")
     assert not dk[0, 2:].any() and not dv[0, 2:].any() and dk[0, :2].any(-1).all()
+
+
+# ----------------------------------------------------------------------- attention
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Nq", [5, 90])
+def test_rows_without_a_finite_score_have_no_gradient(Nq, D):
+    """Finite Q and K whose scores are all below fp32's range: the forward call gives such a row zeros and lse = -inf,
+    as without keys, so it has no part in any gradient."""
+    Hq, Hk, Nk = 2, 1, 300
+    q, k, v = tokens(250, 1, Hq, Hk, Nq, Nk, D)
+    k[:, 64:128] = -1e20
+    q[:, ::3] = 0                                    # scores of zero everywhere
+    q[:, 1::3] = 1e20                                # minus infinity in block 1
+    sel = torch.zeros(Hk, Nq, 2, dtype=torch.int32, device="cuda")
+    sel[:, :, 1] = torch.where(torch.arange(Nq, device="cuda") % 3 == 0, 1, -1)
+    sel[:, 1::3, 0] = 1
+    o, lse = svg.block_attn(q, k, v, sel, 64, False, want_lse=True)
+    assert not o[:, 1::3].any() and (lse[:, 1::3] == -float("inf")).all()
+    assert lse[:, ::3].isfinite().all() and lse[:, 2::3].isfinite().all()
+    do = bf(253, Hq, Nq, D)
+    got = svg.block_attn_backward(do, q, k, v, o, lse, sel, 64, False)
+    gone = sel.clone()
+    gone[:, 1::3] = -1
+    want, bounds = bo.attention_backward(f64(do), f64(q), f64(k), f64(v), f64(o), f64(lse), gone.cpu().numpy(), 64,
+                                         False, [Nk], D ** -0.5)
+    for x, y, z, n in zip(got, want, bounds, ("dq", "dk", "dv")):
+        within(x, y, z, n)
+    assert not got[0][:, 1::3].any()
