@@ -92,6 +92,11 @@ int num_sms() {
   return g_num_sms;
 }
 
+constexpr size_t kMaxSmem = 227 * 1024;      // of a CTA
+
+// Lets a kernel take `bytes` of dynamic shared memory.  The limit is the
+// kernel's, not the launch's: where sizes differ between calls, `bytes` is the
+// largest of them, or a call from another thread could lower it before a launch.
 template <typename F>
 bool set_smem(F kernel, size_t bytes) {
   return cuda_status(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -489,7 +494,7 @@ svg_status svg_select_topp(const float *mu_q, const int32_t *n_q, const float *m
   const dim3 grid((Cq + kSelRows - 1) / kSelRows, BH);
   const int cpl = select_cpl(Ck);
   auto launch = [&](auto kernel) {
-    if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
+    if (!set_smem(kernel, select_smem_bytes(D, kMaxCk))) return SVG_ERR_CUDA;
     kernel<<<grid, kSelRows * 32, smem, s>>>(mu_q, n_q, mu_k, n_k, Cq, Ck, p, scale_d, sel_count, sel_cols);
     return launch_status("select_topp_kernel");
   };
@@ -1030,7 +1035,7 @@ SelectArgs carve_select(void *ws, int BHk, int Nq, int nblk, int D, size_t *byte
   return a;
 }
 
-constexpr size_t kMaxSmem = 227 * 1024, kHalfSmem = (228 * 1024 - 2 * 1024) / 2;   // one CTA per SM; two
+constexpr size_t kHalfSmem = (228 * 1024 - 2 * 1024) / 2;   // two CTAs per SM
 // Tokens of a 128-row tile: as many as fit with their bit sets (fewer only for
 // one or two heads to a key head and thousands of blocks).
 template <typename F>
@@ -1185,7 +1190,7 @@ svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, 
   if (few) {
     auto one = [&](auto kernel) {
       const size_t smem = select_decode_smem(nblk);
-      if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
+      if (!set_smem(kernel, select_decode_smem(kMaxBlocks))) return SVG_ERR_CUDA;
       kernel<<<BHk * Nq, kSelDecodeThreads, smem, s>>>(a);
       return launch_status("block_select_decode_kernel");
     };
@@ -1259,7 +1264,7 @@ svg_status svg_block_attn(const void *q, const void *k, const void *v, int BHq, 
   const dim3 grid(static_cast<unsigned>(ctas), p.splits);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   auto go = [&](auto kernel, int threads, size_t smem) {
-    if (!set_smem(kernel, smem)) return SVG_ERR_CUDA;
+    if (!set_smem(kernel, kMaxSmem)) return SVG_ERR_CUDA;
     kernel<<<grid, threads, smem, s>>>(a);
     return launch_status("block_attn_kernel");
   };
@@ -1350,7 +1355,7 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
   st = launch_status("block_attn_items_kernel");
   if (st != SVG_OK) return st;
   auto go = [&](auto dq_kernel, size_t dq_smem, auto dkv_kernel, size_t dkv_smem, auto join) {
-    if (!set_smem(dq_kernel, dq_smem) || !set_smem(dkv_kernel, dkv_smem)) return SVG_ERR_CUDA;
+    if (!set_smem(dq_kernel, kMaxSmem) || !set_smem(dkv_kernel, kMaxSmem)) return SVG_ERR_CUDA;
     dq_kernel<<<static_cast<unsigned>(ctas), kTcDqThreads, dq_smem, s>>>(a);
     dkv_kernel<<<static_cast<unsigned>(w.max_items), kTcDkvThreads, dkv_smem, s>>>(a);
     join<<<static_cast<unsigned>(tiles), 256, 0, s>>>(a);

@@ -1,4 +1,6 @@
 """GPU tests of the edges of blocks.py, against oracle/block_oracle.py or dense forms in 64 bits."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -116,3 +118,43 @@ def test_rows_without_a_finite_score_have_no_gradient(Nq, D):
     for x, y, z, n in zip(got, want, bounds, ("dq", "dk", "dv")):
         within(x, y, z, n)
     assert not got[0][:, 1::3].any()
+
+
+# ----------------------------------------------------------------------- calls
+def test_two_threads_with_lists_of_different_lengths():
+    """The kernels' shared memory grows with the number of blocks; calls from two threads do not disturb each other."""
+    cases = []
+    for seed, Nk in ((280, 200), (290, 262144)):
+        q, k, v = tokens(seed, 1, 1, 1, 140, Nk, 64)
+        nblk = -(-Nk // 64)
+        sel = (torch.arange(140)[:, None] * 7 + torch.arange(3)) % nblk
+        sel = sel.int().view(1, 140, 3).cuda()
+        mean = svg.block_mean(k, 64)
+        one = bf(seed + 5, 1, 1, 64)
+
+        def run(q=q, k=k, v=v, sel=sel, mean=mean, one=one, Nk=Nk):
+            o, lse = svg.block_attn(q, k, v, sel, 64, False, want_lse=True)
+            s1 = svg.block_select(one, mean, 64, 3, Nk)
+            o1, _ = svg.block_attn(one, k, v, s1, 64)
+            return [o, lse, *svg.block_attn_backward(q, q, k, v, o, lse, sel, 64, False), s1, o1]
+
+        cases.append((run, run()))
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(run, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(400):
+                    got = run()
+                torch.cuda.current_stream().synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+        except Exception as e:  # noqa: BLE001
+            failed.append(repr(e))
+
+    threads = [threading.Thread(target=work, args=c) for c in cases * 2]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
