@@ -349,6 +349,7 @@ svg_status svg_unpermute(const void *xp, const int32_t *perm, int BH, int N, int
  * too: nothing is stored for k and v, which have no row there, while q_out,
  * which has one for every token, gets it.  (Without start, P and cap are
  * checked on the host.)  Norms are formed in fp32, outputs rounded once.
+ * Outputs are other buffers than the inputs.
  */
 svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void *k, const int64_t *k_strides,
                             const void *v, const int64_t *v_strides, const float *w_q, const float *w_k,
@@ -359,7 +360,8 @@ svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void 
 /* Its gradient.  dq_out, dk_out and dv_out are laid out like the outputs, dq,
  * dk and dv like the inputs (strided views); dw_q, dw_k [D] fp32 (NULL to
  * skip) are sums over all rows, in a fixed order.  Rows that the forward call
- * makes zero or does not store get zeros. */
+ * makes zero or does not store get zeros.  dq may be q and dk k, with the same
+ * strides; otherwise outputs are other buffers than the inputs. */
 size_t svg_qk_norm_rope_backward_workspace_size(int B, int N, int Hq, int Hk, int D);
 svg_status svg_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *dv_out, const void *q,
                                      const int64_t *q_strides, const void *k, const int64_t *k_strides,

@@ -888,7 +888,7 @@ svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void 
   if (st != SVG_OK) return st;
   for (int t = 0; t < 3; ++t) {
     if (a.heads[t] == 0) continue;
-    if (!y[t] || !aligned(y[t], 16) || y[t] == x[t]) return SVG_ERR_INVALID_ARG;
+    if (!y[t] || !aligned(y[t], 16) || y[t] == q || y[t] == k || y[t] == v) return SVG_ERR_INVALID_ARG;
     if (t > 0 && !start && cap < N) return SVG_ERR_INVALID_ARG;
     a.y[t] = static_cast<__nv_bfloat16 *>(y[t]);
     for (int u = 0; u < t; ++u)
@@ -947,7 +947,12 @@ svg_status svg_qk_norm_rope_backward(const void *dq_out, const void *dk_out, con
     if (a.heads[t] == 0) continue;
     if (!dy[t] || !dx[t] || !aligned(dy[t], 16) || !aligned(dx[t], 16) || !rope_strides_ok(ds[t]))
       return SVG_ERR_INVALID_ARG;
-    if (dx[t] == dy[t]) return SVG_ERR_INVALID_ARG;
+    // A thread group reads its row of x before it writes there, so dx may be x
+    // itself; every other tensor is read by others.
+    if (dx[t] == dq_out || dx[t] == dk_out || dx[t] == dv_out) return SVG_ERR_INVALID_ARG;
+    if ((t != 0 && dx[t] == q) || (t != 1 && dx[t] == k)) return SVG_ERR_INVALID_ARG;
+    if (t != 2 && dx[t] == x[t] && (ds[t][0] != xs[t][0] || ds[t][1] != xs[t][1] || ds[t][2] != xs[t][2]))
+      return SVG_ERR_INVALID_ARG;
     for (int u = 0; u < t; ++u)
       if (a.heads[u] != 0 && dx[u] == dx[t]) return SVG_ERR_INVALID_ARG;
     if (t > 0 && !start && cap < N) return SVG_ERR_INVALID_ARG;

@@ -92,6 +92,16 @@ def test_tokens_beyond_the_buffer_but_in_the_table():
     assert not dk[0, 2:].any() and not dv[0, 2:].any() and dk[0, :2].any(-1).all()
 
 
+def test_a_gradient_may_replace_its_input():
+    B, N, H, D = 2, 37, 3, 128
+    q, k, v, w_q, w_k = rope_inputs(B, N, H, H, D, seed=235)
+    cos, sin = svg.rope_table((N,), D)
+    dy = [bf(238 + i, B * H, N, D) for i in range(3)]
+    want = svg.qk_norm_rope_backward(*dy, q, k, w_q, w_k, cos, sin)
+    got = svg.qk_norm_rope_backward(*dy, q, k, w_q, w_k, cos, sin, dq=q, dk=k, dv=v)     # slices of one buffer
+    assert got[0] is q and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 # ----------------------------------------------------------------------- attention
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Nq", [5, 90])
