@@ -168,3 +168,49 @@ def test_two_threads_with_lists_of_different_lengths():
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+def test_inputs_that_require_grad_are_refused():
+    """No call records a gradient, so none is lost in silence; under no_grad, and in a Function, they run."""
+    q, k, v, w_q, w_k = rope_inputs(1, 6, 2, 1, 64, seed=300)
+    want = svg.qk_norm_rope(q, k, v, w_q, w_k)
+    par = torch.nn.Parameter(w_q)
+    leaf = q.detach().clone().requires_grad_()
+    for args in ((leaf, k, v, w_q, w_k), (q, k, v, par, w_k), (q, k.detach().clone().requires_grad_(), v)):
+        with pytest.raises(ValueError, match="qk_norm_rope_backward"):
+            svg.qk_norm_rope(*args)
+    with torch.no_grad():
+        got = svg.qk_norm_rope(leaf, k, v, par, w_k)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    qh, kh, vh = tokens(301, 1, 2, 1, 6, 6, 64)
+    sel = torch.zeros(1, 6, 1, dtype=torch.int32, device="cuda")
+    o, lse = svg.block_attn(qh, kh, vh, sel, 64, want_lse=True)
+    for i in range(3):
+        x = [t.clone().requires_grad_() if i == j else t for j, t in enumerate((qh, kh, vh))]
+        with pytest.raises(ValueError, match="block_attn_backward"):
+            svg.block_attn(*x, sel, 64)
+        with pytest.raises(ValueError, match="backward"):
+            svg.block_attention(*x, 64, 1, 0, 1)
+    with pytest.raises(ValueError, match="detach"):
+        svg.block_mean(kh.clone().requires_grad_(), 64)
+
+    class Attend(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, v):
+            o, lse = svg.block_attn(q, k, v, sel, 64, want_lse=True)
+            ctx.save_for_backward(q, k, v, o, lse)
+            return o
+
+        @staticmethod
+        def backward(ctx, do):
+            return svg.block_attn_backward(do.contiguous(), *ctx.saved_tensors, sel, 64)
+
+    leaves = [t.clone().requires_grad_() for t in (qh, kh, vh)]
+    y = Attend.apply(*leaves)
+    do = bf(305, 2, 6, 64)
+    y.backward(do)
+    assert torch.equal(y, o)
+    # lists carry no gradient, so they may be made from such inputs; so may gradients by hand
+    assert torch.equal(svg.block_select(leaves[0], svg.block_mean(kh, 64), 64, 1, 6, 0, 1), sel)
+    for a, b in zip(leaves, svg.block_attn_backward(do, *leaves, o, lse, sel, 64)):
+        assert torch.equal(a.grad, b)
