@@ -204,8 +204,8 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
 
 // grid (token tiles, head chunks): one CTA stays with one chunk, so that its
 // threads sum dw of one tensor.  The next head's rows are on their way while a
-// head is computed.  Sums run in fp32 over a thread's rows (a hundred or so)
-// and a CTA's groups, and in fp64 over the CTAs.
+// head is computed.  Sums run in fp32 over a thread's rows (at most 256: the
+// host's choice of tiles) and a CTA's groups, and in fp64 over the CTAs.
 constexpr int kRopeBackThreads = 128;
 
 template <int D, bool INTER>

@@ -862,12 +862,16 @@ void rope_chunks(RopeArgs &a, int hpt) {
 // Heads of a CTA's chunk in the gradient.
 constexpr int kRopeBackwardHeads = 16;
 // Token tiles: each CTA goes over as many as leave about 4 waves of CTAs (4 per
-// SM), all the same number; this also bounds the partial sums of dw.
+// SM), all the same number, and at most 16: with 16 heads to a chunk, a thread
+// then adds 256 rows of dw in fp32, whatever the number of tokens (more than
+// 600,000 tokens x chunks at D = 128 take more waves instead).
+constexpr int64_t kRopeBackwardTiles = 16;
 int rope_backward_tiles(int B, int N, int D, int chunks) {
   const int64_t groups = kRopeBackThreads / (D / 16);
   const int64_t all = (static_cast<int64_t>(B) * N + groups - 1) / groups;
   const int64_t most = 4ll * 4 * num_sms();
-  const int64_t each = (all * chunks + most - 1) / most;
+  int64_t each = (all * chunks + most - 1) / most;
+  if (each > kRopeBackwardTiles) each = kRopeBackwardTiles;
   return static_cast<int>((all + each - 1) / each);
 }
 }  // namespace

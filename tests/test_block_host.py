@@ -45,3 +45,15 @@ def test_a_rotation_does_not_write_over_any_input(lib):
     assert backward(dq=k) == 1 and backward(dk=q) == 1 and backward(dv=q) == 1 and backward(dv=k) == 1
     assert backward(dq=q) == 3 and backward(dk=k) == 3  # a row's gradient may replace it
     assert backward(dq=q, dqs=(ctypes.c_int64 * 3)(512, 64, 512)) == 1
+
+
+@pytest.mark.parametrize("heads,D", [(1, 64), (3, 64), (16, 64), (40, 128), (17, 128)])
+@pytest.mark.parametrize("tokens", [1, 10_002, 524_160, 4_000_000])
+def test_sums_of_the_weight_gradient_stay_short(lib, heads, D, tokens):
+    """A thread adds at most 256 rows in fp32 before its sum goes on in fp64, whatever the number of tokens: there
+    are that many partial rows."""
+    size = lib.svg_qk_norm_rope_backward_workspace_size(1, tokens, heads, 0, D)
+    chunks = -(-heads // 16)
+    tiles = size // (4 * D * chunks)                  # (sizes are whole multiples of 256 bytes)
+    groups = 128 // (D // 16)
+    assert tiles * groups * 16 >= tokens

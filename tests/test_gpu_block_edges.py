@@ -102,6 +102,23 @@ def test_a_gradient_may_replace_its_input():
     assert got[0] is q and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_weight_gradient_over_many_tokens():
+    """Sums over 400,000 tokens with a mean, so that roundings add up: at most 256 fp32 additions to a thread's sum,
+    8 to a CTA's, fp64 behind them."""
+    N, H, D = 400_000, 3, 64
+    g = torch.Generator(device="cuda").manual_seed(240)
+    q = (torch.randn(1, N, H, D, generator=g, device="cuda") + 2.0).to(BF)
+    dqo = (torch.rand(H, N, D, generator=g, device="cuda") + 0.5).to(BF)
+    _, _, _, dw, _ = svg.qk_norm_rope_backward(dqo, None, None, q, eps=1e-5)
+    want = torch.zeros(D, dtype=torch.float64, device="cuda")
+    for a in range(0, N, 50_000):
+        x = q[0, a:a + 50_000].double()
+        n = x / (x.pow(2).mean(-1, keepdim=True) + 1e-5).sqrt()
+        want += (n * dqo[:, a:a + 50_000].double().transpose(0, 1)).sum((0, 1))
+    # a product of a value, rsqrt (2 ulp of a sum of 64 squares) and u: below 64 + 8 half steps, all terms positive
+    assert ((dw.double() - want).abs() <= (256 + 32 + 72) * bo.HALF_F32 * want).all()
+
+
 # ----------------------------------------------------------------------- attention
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("Nq", [5, 90])
