@@ -208,7 +208,8 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, v: Optional[
     output); w_q, w_k [D] fp32 or None (ones); cos, sin [P, D/2] fp32 or None (no rotation), one row per position;
     start [B] int32: position of each sequence's token 0 (None: 0).  q_out [B*Hq, N, D]; k_out, v_out
     [B*Hk, cap, D]: token n goes to row start[b] + n, other rows stay as they are (None: new buffers of N rows,
-    without start only).  Negative positions are padding (see svg_qk_norm_rope).  Returns (q_out, k_out, v_out).
+    without start only; a new v_out has k_out's rows, zeros behind the N).  Negative positions are padding (see
+    svg_qk_norm_rope).  Returns (q_out, k_out, v_out).
     """
     lib = load_library()
     _constant("qk_norm_rope", "call it under torch.no_grad() and qk_norm_rope_backward for the gradient",
@@ -229,6 +230,8 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, v: Optional[
             cap = _cap(k_out, "k_out", B * Hk, D, N)
         if v is not None:
             pv, sv = _view(v, "v", (B, N, Hk, D))
+            if v_out is None and cap > N:             # beside a longer k_out: rows that nobody writes are zero
+                v_out = torch.zeros((B * Hk, cap, D), dtype=bf, device=dev)
             v_out = _out(v_out, "v_out", (B * Hk, cap, D), bf, dev)
         _check("svg_qk_norm_rope", lib.svg_qk_norm_rope(
             pq, sq, pk, sk, pv, sv, _ptr(w_q), _ptr(w_k), _ptr(cos), _ptr(sin), P, B, N, Hq, Hk, D, float(eps),

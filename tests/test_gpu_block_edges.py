@@ -92,6 +92,16 @@ def test_tokens_beyond_the_buffer_but_in_the_table():
     assert not dk[0, 2:].any() and not dv[0, 2:].any() and dk[0, :2].any(-1).all()
 
 
+def test_a_new_v_buffer_beside_a_longer_k_buffer_holds_nothing_else():
+    N, H, D, cap = 4, 2, 64, 9
+    _, k, v, _, _ = rope_inputs(1, N, H, H, D, seed=230)
+    stale = [torch.full((H, cap, D), 7.0, dtype=BF, device="cuda") for _ in range(4)]
+    del stale                                        # the allocator hands these out again
+    ko = torch.zeros(H, cap, D, dtype=BF, device="cuda")
+    _, _, vo = svg.qk_norm_rope(k, k, v, k_out=ko)
+    assert torch.equal(vo[:, :N], v[0].transpose(0, 1)) and not vo[:, N:].any()
+
+
 def test_a_gradient_may_replace_its_input():
     B, N, H, D = 2, 37, 3, 128
     q, k, v, w_q, w_k = rope_inputs(B, N, H, H, D, seed=235)
