@@ -116,7 +116,7 @@ __device__ __forceinline__ int mark_blocks(const BlockAttnArgs &a, int head, int
 }
 
 // Bytes of the bit sets, their union and its list.
-__host__ __device__ inline size_t mark_bytes(int tokens, int nblk) {
+__host__ __device__ constexpr size_t mark_bytes(int tokens, int nblk) {
   const size_t W = (nblk + 31) / 32;
   return (static_cast<size_t>(tokens) + 1) * W * 4 + static_cast<size_t>(nblk) * 2;
 }
@@ -174,7 +174,7 @@ __device__ __forceinline__ BaRow ba_row(const BlockAttnArgs &a, int head, int le
 
 // Shared memory: rows of K and V, then the list's length, bit sets, list.
 template <int D>
-__host__ __device__ inline size_t block_attn_smem(int rows, int tokens, int nblk) {
+__host__ __device__ constexpr size_t block_attn_smem(int rows, int tokens, int nblk) {
   return static_cast<size_t>(rows) * D * 2 + 16 + mark_bytes(tokens, nblk);
 }
 

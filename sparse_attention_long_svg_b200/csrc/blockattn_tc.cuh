@@ -128,7 +128,7 @@ __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t parity, uin
 // Shared memory of the two query-major kernels: `operands` 128-row tiles, two
 // stages of K and V, barriers, bit sets, block list.
 template <int D>
-__host__ __device__ inline size_t tc_smem(int operands, int tokens, int nblk) {
+__host__ __device__ constexpr size_t tc_smem(int operands, int tokens, int nblk) {
   return static_cast<size_t>(operands) * kTcRows * D * 2 + 4ull * kBaTile * D * 2 + 192 + mark_bytes(tokens, nblk);
 }
 
@@ -476,7 +476,7 @@ struct TcDqBars {                      // at most 128 bytes
 };
 
 template <int D>
-__host__ __device__ inline size_t tc_dq_smem(int k_stages, int tokens, int nblk) {
+__host__ __device__ constexpr size_t tc_dq_smem(int k_stages, int tokens, int nblk) {
   return 2ull * kTcRows * D * 2 + (1ull + k_stages) * kBaTile * D * 2 + 128 + mark_bytes(tokens, nblk);
 }
 
@@ -745,7 +745,7 @@ struct TcDkvBars {                     // at most 256 bytes
 };
 
 template <int D>
-__host__ __device__ inline size_t tc_dkv_smem(int item_tokens) {
+__host__ __device__ constexpr size_t tc_dkv_smem(int item_tokens) {
   return 2ull * kBaTile * D * 2 + 4ull * kTcRows * D * 2 + 2ull * kTcRows * 128 + 256 + static_cast<size_t>(item_tokens) * 4;
 }
 

@@ -1045,14 +1045,19 @@ SelectArgs carve_select(void *ws, int BHk, int Nq, int nblk, int D, size_t *byte
 }
 
 constexpr size_t kHalfSmem = (228 * 1024 - 2 * 1024) / 2;   // two CTAs per SM
-// Tokens of a 128-row tile: as many as fit with their bit sets (fewer only for
-// one or two heads to a key head and thousands of blocks).
-template <typename F>
-int tile_tokens(int G, F smem) {
-  int t = kTcRows / G;
-  while (smem(t) > kMaxSmem) t = (t + 1) / 2;
-  return t;
-}
+
+// Gradient: rows of one work item (a key tile's queries beyond it go to more).
+constexpr int kBaItemRows = 4096;
+
+// Tokens of a 128-row tile.  Their bit sets and the block list fit beside the
+// operands at any number of blocks; what long lists leave no room for is an SM's
+// second CTA (D = 128: beyond 928 blocks where G = 1, 1,696 where G = 2, 2,800
+// where G = 4).
+constexpr int tile_tokens(int G) { return kTcRows / G; }
+static_assert(tc_smem<128>(1, kTcRows, kMaxBlocks) <= kMaxSmem && tc_dq_smem<128>(1, kTcRows, kMaxBlocks) <= kMaxSmem &&
+                  tc_dkv_smem<128>(kBaItemRows) <= kMaxSmem &&
+                  block_attn_smem<128>(kFewRows, 16, kMaxBlocks) <= kMaxSmem,
+              "the longest lists and items must fit one CTA to an SM");
 
 struct BlockAttnPlan {
   bool few;
@@ -1064,7 +1069,7 @@ BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int 
   BlockAttnPlan p;
   const int per = 16 / (BHq / BHk);
   p.few = Nq <= per;
-  p.tokens = p.few ? per : tile_tokens(BHq / BHk, [&](int t) { return tc_smem<128>(1, t, nblk); });
+  p.tokens = p.few ? per : tile_tokens(BHq / BHk);
   p.tiles = (Nq + p.tokens - 1) / p.tokens;
   const int64_t ctas = static_cast<int64_t>(BHk) * p.tiles;
   const int64_t listed = static_cast<int64_t>(Nq < p.tokens ? Nq : p.tokens) * topk;
@@ -1077,8 +1082,6 @@ BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int 
   return p;
 }
 
-// Gradient: rows of one work item (a key tile's queries beyond it go to more).
-constexpr int kBaItemRows = 4096;
 struct BlockGradWs {
   float *delta, *part_kv;
   uint32_t *rev;
@@ -1330,7 +1333,7 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
   auto dq_bytes = [&](int stages, int t) {
     return D == 128 ? tc_dq_smem<128>(stages, t, nblk) : tc_dq_smem<64>(stages, t, nblk);
   };
-  const int tokens = tile_tokens(BHq / BHk, [&](int t) { return dq_bytes(1, t); });
+  const int tokens = tile_tokens(BHq / BHk);
   // A second stage of K where two CTAs still share an SM (D = 128: lists of up
   // to a few hundred blocks).
   const int k_stages = dq_bytes(2, tokens) <= kHalfSmem ? 2 : 1;
