@@ -157,6 +157,74 @@ def test_rows_without_a_finite_score_have_no_gradient(Nq, D):
     assert not got[0][:, 1::3].any()
 
 
+@pytest.mark.parametrize("G,N,items", [(16, 700, 3), (4, 2200, 3)])
+def test_gradient_of_key_tiles_with_three_items(G, N, items):
+    """A block whose queries fill more than two work items of 4,096 rows: their sums are joined in order."""
+    Hk, D = 2, 64
+    Hq = Hk * G
+    assert -(-N // (4096 // G)) == items
+    q, k, v = tokens(260, 1, Hq, Hk, N, N, D)
+    sel = torch.zeros(Hk, N, 2, dtype=torch.int32, device="cuda")
+    sel[:, :, 1] = torch.arange(N, device="cuda") // 64
+    o, lse = svg.block_attn(q, k, v, sel, 64, want_lse=True)
+    do = bf(263, Hq, N, D)
+    got = svg.block_attn_backward(do, q, k, v, o, lse, sel, 64)
+    want, bounds = dense_gradient(do, q, k, v, o, lse, sel, 64, True)
+    for x, y, z, n in zip(got, want, bounds, ("dq", "dk", "dv")):
+        assert ((x.double() - y).abs() <= z).all(), (n, float(((x.double() - y).abs() - z).max()))
+
+
+def dense_gradient(do, q, k, v, o, lse, sel, block, causal):
+    """Gradients in 64 bits on the device, and their bounds (see oracle/block_oracle.py: attention_backward)."""
+    Hq, N, D = q.shape
+    Hk, Nk, _ = k.shape
+    G, nblk, scale = Hq // Hk, -(-Nk // block), D ** -0.5
+    hit = torch.zeros(Hk, N, nblk + 1, dtype=torch.bool, device="cuda")
+    hit.scatter_(2, torch.where(sel < 0, nblk, sel).long(), True)
+    mask = hit[:, :, :nblk].repeat_interleave(block, 2)[:, :, :Nk]
+    if causal:
+        mask &= torch.arange(Nk, device="cuda") <= torch.arange(Nk - N, Nk, device="cuda")[:, None]
+    out = [torch.zeros_like(x, dtype=torch.float64) for x in (q, k, v, q, k, v)]
+    dq, dk, dv, bq, bk, bv = out
+    for h in range(Hq):
+        j = h // G
+        qq, kk, vv, g, y = q[h].double(), k[j].double(), v[j].double(), do[h].double(), o[h].double()
+        s = qq @ kk.T * scale
+        p = (s - lse[h].double()[:, None]).exp().masked_fill(~mask[j], 0)
+        ds = p * (g @ vv.T - (g * y).sum(-1, keepdim=True))
+        dq[h] = ds @ kk * scale
+        dk[j] += ds.T @ qq * scale
+        dv[j] += p.T @ g
+        # scores and the exponent's argument in fp32, dP and delta too; P and dS as bf16 operands
+        es = D * bo.HALF_F32 * scale * (qq.abs() @ kk.abs().T).amax(-1, keepdim=True) + 8 * bo.HALF_F32 * (
+            1 + s.abs().amax(-1, keepdim=True))
+        ed = D * bo.HALF_F32 * (g.abs() @ vv.abs().T + (g.abs() * y.abs()).sum(-1, keepdim=True))
+        eds = (bo.HALF_BF16 * 1.01 + 2 * es) * ds.abs() + 2 * p * ed
+        ep = (bo.HALF_BF16 * 1.01 + 2 * es) * p
+        bq[h] = eds @ kk.abs() * scale
+        bk[j] += eds.T @ qq.abs() * scale
+        bv[j] += ep.T @ g.abs()
+    return out[:3], [b * (1 + N * G * bo.HALF_F32) + bo.HALF_BF16 * x.abs() * 1.01 + 1e-30
+                     for b, x in zip(out[3:], out[:3])]
+
+
+@pytest.mark.parametrize("G,D,causal", [(5, 128, True), (1, 64, False)])
+def test_all_gradients_of_many_tiles(G, D, causal):
+    """dQ, dK and dV of hundreds of tiles that share the GPU, against dense attention in 64 bits."""
+    Hk, N, topk = 4, 3000, 12
+    Hq = Hk * G
+    q, k, v = tokens(270, 1, Hq, Hk, N, N, D)
+    g = torch.Generator().manual_seed(271)
+    near = torch.arange(N)[None, :, None] // 64 - torch.arange(4)
+    sel = torch.cat([near.expand(Hk, N, 4), torch.randint(0, 47, (Hk, N, topk - 4), generator=g)], 2).int().cuda()
+    o, lse = svg.block_attn(q, k, v, sel, 64, causal, want_lse=True)
+    do = bf(273, Hq, N, D)
+    got = svg.block_attn_backward(do, q, k, v, o, lse, sel, 64, causal)
+    want, bounds = dense_gradient(do, q, k, v, o, lse, sel, 64, causal)
+    for x, y, z, n in zip(got, want, bounds, ("dq", "dk", "dv")):
+        assert ((x.double() - y).abs() <= z).all(), (n, float(((x.double() - y).abs() - z).max()))
+
+
 # ----------------------------------------------------------------------- calls
 def test_two_threads_with_lists_of_different_lengths():
     """The kernels' shared memory grows with the number of blocks; calls from two threads do not disturb each other."""
