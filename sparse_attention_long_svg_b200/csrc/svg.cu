@@ -1159,10 +1159,10 @@ svg_status svg_block_mean(const void *k, int BHk, int B, int Nk, int D, int bloc
 }
 
 size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int D, int block) {
-  if (BHk <= 0 || Nq <= 0 || Nk <= 0 || D <= 0 || block <= 0 || !sizes_ok(BHk, Nq) || !sizes_ok(BHk, Nk)) return 0;
-  if (select_few(Nq)) return 0;
+  int nblk;
+  if (block_shapes(BHk, BHk, 1, Nq, Nk, D, block, &nblk) != SVG_OK || select_few(Nq)) return 0;
   size_t bytes = 0;
-  carve_select(nullptr, BHk, Nq, (Nk + block - 1) / block, D, &bytes);
+  carve_select(nullptr, BHk, Nq, nblk, D, &bytes);
   return bytes;
 }
 

@@ -57,3 +57,15 @@ def test_sums_of_the_weight_gradient_stay_short(lib, heads, D, tokens):
     tiles = size // (4 * D * chunks)                  # (sizes are whole multiples of 256 bytes)
     groups = 128 // (D // 16)
     assert tiles * groups * 16 >= tokens
+
+
+def test_refused_shapes_ask_for_no_workspace(lib):
+    """A call that will be refused does not make the caller allocate first."""
+    size = lib.svg_block_select_workspace_size
+    assert size(8, 100, 4096, 128, 64) > 0 and size(8, 100, 4096, 128, 128) > 0
+    assert size(8, 100, 4096, 128, 32) == 0 and size(8, 100, 4096, 96, 64) == 0
+    assert size(8, 100, 64 * 4096 + 1, 128, 64) == 0 and size(8, 100, 1 << 20, 128, 1) == 0
+    assert size(8, 4, 4096, 128, 64) == 0             # few queries need none
+    for f in (lib.svg_block_attn_workspace_size, lib.svg_block_attn_backward_workspace_size):
+        assert f(8, 8, 1, 4096, 128, 16, 32) == 0 and f(8, 8, 1, 64 * 4096 + 1, 128, 16, 64) == 0
+        assert f(8, 3, 1, 4096, 128, 16, 64) == 0 and f(8, 8, 1, 4096, 128, 0, 64) == 0
