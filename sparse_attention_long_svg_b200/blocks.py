@@ -56,10 +56,9 @@ def _side(stream, *tensors):
 
 def _constant(call: str, instead: str, *tensors):
     """Refuses tensors whose gradient would be lost."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{call} records no gradient, but an input requires grad: {instead}")
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{call} records no gradient, but an input requires grad: {instead}")
 
 
 def _device() -> int:
@@ -213,7 +212,7 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, v: Optional[
     """
     lib = load_library()
     _constant("qk_norm_rope", "call it under torch.no_grad() and qk_norm_rope_backward for the gradient",
-              q, k, v, w_q, w_k, cos, sin, q_out, k_out, v_out)
+              q, k, v, w_q, w_k)
     B, N, Hq, Hk, D, P = _rope_common(q, k, v, w_q, w_k, cos, sin, start)
     with _side(stream, q, k, v, w_q, w_k, cos, sin, start, q_out, k_out, v_out):
         dev, bf = q.device, torch.bfloat16
@@ -295,7 +294,7 @@ def block_mean(k: torch.Tensor, block: int, kv_len: Optional[torch.Tensor] = Non
     kv_len [B] int32: keys in use (None: all).  With `new` > 0 only the blocks that hold any of a sequence's last
     `new` keys are formed, in place in `mean` (the means of a cache after a decoding step)."""
     lib = load_library()
-    _constant("block_mean", "give it k.detach(): means serve the choice of blocks, which is constant", k, mean)
+    _constant("block_mean", "give it k.detach(): means serve the choice of blocks, which is constant", k)
     _need(k, "k", torch.bfloat16, 3)
     BHk, Nk, D = k.shape
     B = _seqs(kv_len, BHk)
@@ -364,7 +363,7 @@ def block_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, sel: torch.Ten
     q [BHq, Nq, D], k, v [BHk, Nk, D] bf16, sel [BHk, Nq, topk] int32 (block_select; -1 is passed over).  Query
     head h reads key head h // (BHq / BHk).  A query without a visible key gets zeros.  Returns (o, lse or None)."""
     lib = load_library()
-    _constant("block_attn", _ATTN_INSTEAD, q, k, v, o, lse)
+    _constant("block_attn", _ATTN_INSTEAD, q, k, v)
     BHq, BHk, B, Nq, Nk, D, topk = _attn_shapes(q, k, v, sel, kv_len)
     with _side(stream, q, k, v, sel, kv_len, o, lse, workspace):
         o = _out(o, "o", (BHq, Nq, D), torch.bfloat16, q.device)
@@ -411,7 +410,7 @@ def block_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, block: in
 
     `mean` with `new` > 0: the means of a cache, brought up to date for its last `new` keys; else all are formed
     (into `mean` if given).  Returns (o, lse or None, sel, mean)."""
-    _constant("block_attention", _ATTN_INSTEAD, q, k, v, mean)
+    _constant("block_attention", _ATTN_INSTEAD, q, k, v)
     mean = block_mean(k, block, kv_len, new, mean, stream)
     sel = block_select(q, mean, block, topk, k.shape[1], sink, local, causal, kv_len, stream=stream)
     o, lse = block_attn(q, k, v, sel, block, causal, scale, kv_len, want_lse=want_lse, stream=stream)
