@@ -1006,9 +1006,17 @@ svg_status block_shapes(int BHq, int BHk, int B, int Nq, int Nk, int D, int bloc
   return *nblk > kMaxBlocks ? SVG_ERR_UNSUPPORTED : SVG_OK;
 }
 
-// block_select: few queries take the kernel with one CTA per query (it reads a
-// head's means once per query), more the one with 64 queries per CTA.
-bool select_few(int Nq) { return Nq <= 4; }
+// block_select: few queries take the kernel with one CTA per query, which reads
+// a head's means once per query; more the one with 64 queries per CTA, whose few
+// CTAs would leave most SMs idle.  The first grows with heads x queries, the
+// second hardly until its CTAs fill the GPU.  us, first / second kernel, D = 128:
+//   key heads  blocks  4 queries     8          16          32
+//          8      512  18 /  38   16 / 38    18 /  38    31 /  40
+//          8     2048  27 /  79   25 / 81    27 /  83    45 /  83
+//         32      512  20 /  40   31 / 40    49 /  42    84 /  44
+//         32     2048  27 /  89   43 / 91    80 /  93   135 / 101
+//        128     2048  84 / 128  139 / 132  262 / 142   510 / 165
+bool select_few(int BHk, int Nq) { return Nq <= 4 || (Nq <= 32 && static_cast<int64_t>(BHk) * Nq <= 512); }
 int64_t select_items(int BHk, int Nq) { return static_cast<int64_t>(BHk) * ((Nq + kSelTile - 1) / kSelTile); }
 // Items of a part: a multiple of what runs at a time (3 per SM) whose scores take
 // at most 256 MiB.  32,760 queries x 8 key heads x 512 blocks: 64 MiB, which
@@ -1160,7 +1168,7 @@ svg_status svg_block_mean(const void *k, int BHk, int B, int Nk, int D, int bloc
 
 size_t svg_block_select_workspace_size(int BHk, int Nq, int Nk, int D, int block) {
   int nblk;
-  if (block_shapes(BHk, BHk, 1, Nq, Nk, D, block, &nblk) != SVG_OK || select_few(Nq)) return 0;
+  if (block_shapes(BHk, BHk, 1, Nq, Nk, D, block, &nblk) != SVG_OK || select_few(BHk, Nq)) return 0;
   size_t bytes = 0;
   carve_select(nullptr, BHk, Nq, nblk, D, &bytes);
   return bytes;
@@ -1180,7 +1188,7 @@ svg_status svg_block_select(const void *q, const float *mean, int BHq, int BHk, 
   const size_t need = svg_block_select_workspace_size(BHk, Nq, Nk, D, block);
   if (need > 0 && !ws) return SVG_ERR_INVALID_ARG;
   if (ws_bytes < need) return SVG_ERR_WORKSPACE;
-  const bool few = select_few(Nq);
+  const bool few = select_few(BHk, Nq);
   size_t used = 0;
   SelectArgs a = few ? SelectArgs{} : carve_select(ws, BHk, Nq, nblk, D, &used);
   a.q = static_cast<const __nv_bfloat16 *>(q);

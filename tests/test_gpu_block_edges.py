@@ -37,6 +37,18 @@ def test_selection_of_scores_beyond_fp32(Nq, nblk, topk):
     assert np.array_equal(sel.cpu().numpy(), want), np.argwhere(sel.cpu().numpy() != want)[:5]
 
 
+@pytest.mark.parametrize("B,Hq,Hk,Nq", [(1, 32, 16, 32), (1, 17, 17, 32), (4, 120, 30, 5), (3, 34, 34, 5), (1, 15, 15, 33)])
+def test_selection_by_either_kernel(B, Hq, Hk, Nq):
+    """Both sides of the switch between a CTA per query and a CTA per 64 queries."""
+    D, Nk, lens = 64, 9000, (9000, 20, 4097, 640)[:B]
+    q = bf(205, B * Hq, Nq, D)
+    mean = torch.randn(B * Hk, -(-Nk // 64), D, generator=torch.Generator().manual_seed(206)).cuda()
+    mean[:, 6] = mean[:, 4] * (1 + 2.0 ** -22)
+    sel = svg.block_select(q, mean, 64, 12, Nk, 1, 2, True, kv_len=i32(*lens))
+    want = bo.select_blocks(f64(q), f64(mean), 64, 12, 1, 2, True, [n for n in lens for _ in range(Hk)])
+    assert np.array_equal(sel.cpu().numpy(), want), np.argwhere(sel.cpu().numpy() != want)[:5]
+
+
 # ----------------------------------------------------------------------- norm and rotation
 def test_tokens_beyond_the_table_leave_every_cache_row_alone():
     """P <= position < cap: as for padding, Q's row is zero and neither K nor V is stored; the gradient is zero."""
