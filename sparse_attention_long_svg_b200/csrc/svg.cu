@@ -899,11 +899,17 @@ svg_status svg_qk_norm_rope(const void *q, const int64_t *q_strides, const void 
       if (a.heads[u] != 0 && y[u] == y[t]) return SVG_ERR_INVALID_ARG;
   }
   if (cos && !start && P < N) return SVG_ERR_INVALID_ARG;
-  // One head per thread while that leaves the GPU short of threads, else 4 in
-  // flight of a chunk of 8 that shares its angles.
-  const int64_t rows = static_cast<int64_t>(B) * N * (a.heads[0] + a.heads[1] + a.heads[2]);
-  const bool wide = rows * (D / 16) >= static_cast<int64_t>(num_sms()) * 2048 * 4;
-  rope_chunks(a, wide ? 8 : 1);
+  // Large calls: chunks of 8 heads that share their angles, 4 in flight, with
+  // streaming stores; others (their outputs stay in L2) one head per thread.  us,
+  // chunks / one head, D = 128, 512,000 rows: 55 / 84 with 40 and 8 heads, 61 / 82
+  // with 12 and 12, 90 / 86 with 8 and 1, 234 / 88 with 1 and 1, where a chunk's
+  // places are mostly empty; 4,000 rows: 10.2 / 8.2.  At 128,000 rows, below the
+  // border, 20.5 / 26.6.
+  const int64_t heads = a.heads[0] + a.heads[1] + a.heads[2], rows = static_cast<int64_t>(B) * N * heads;
+  rope_chunks(a, 8);
+  const bool wide = rows * (D / 16) >= static_cast<int64_t>(num_sms()) * 2048 * 4 &&
+                    3 * heads >= 2 * 8 * (a.chunks[0] + a.chunks[1] + a.chunks[2]);
+  if (!wide) rope_chunks(a, 1);
   const int64_t groups = static_cast<int64_t>(B) * N * (a.chunks[0] + a.chunks[1] + a.chunks[2]);
   const int64_t per = kRopeThreads / (D / 16);
   const unsigned grid = static_cast<unsigned>((groups + per - 1) / per);

@@ -104,6 +104,21 @@ def test_tokens_beyond_the_buffer_but_in_the_table():
     assert not dk[0, 2:].any() and not dv[0, 2:].any() and dk[0, :2].any(-1).all()
 
 
+def test_many_rows_of_few_heads():
+    """Large calls whose chunks of 8 heads would be mostly empty: each row is what a small call gives it."""
+    N, D = 55_000, 128
+    q, k, v, w_q, w_k = rope_inputs(1, N, 1, 1, D, seed=228)
+    cos, sin = svg.rope_table((N,), D)
+    assert N * 3 * D // 16 >= 148 * 2048 * 4         # threads of a large call
+    got = svg.qk_norm_rope(q, k, v, w_q, w_k, cos, sin)
+    for a in (0, 30_000, 54_900):
+        part = slice(a, a + 100)
+        few = svg.qk_norm_rope(q[:, part], k[:, part], v[:, part], w_q, w_k, cos[part].contiguous(),
+                               sin[part].contiguous())
+        for x, y in zip(got, few):
+            assert torch.equal(x[:, part], y)
+
+
 def test_a_new_v_buffer_beside_a_longer_k_buffer_holds_nothing_else():
     N, H, D, cap = 4, 2, 64, 9
     _, k, v, _, _ = rope_inputs(1, N, H, H, D, seed=230)
