@@ -261,7 +261,7 @@ __device__ __noinline__ uint32_t rank_near(const SelectArgs &a, const int *near,
 //
 // The ordinary one keeps the row in registers (VPL places; forced blocks and
 // places without one are NaN, which no comparison takes) and finds the last
-// place's score from the lanes' largest ones (up to 32 places), or by bisection.
+// place's score from the lanes' largest ones (few places), or by bisection.
 // Returns false, with nothing written, for rows that are flat (more than 32
 // near the border) or whose scores have no finite bound.
 template <int D, int VPL>
@@ -302,11 +302,15 @@ __device__ __forceinline__ bool select_row(const SelectArgs &a, const float *s, 
       best = ((lane & k) == 0) == ((lane & o) == 0) ? fmaxf(best, x) : fminf(best, x);
     }
   const float top = __shfl_sync(all, best, 0);
-  // The need-th of them is a lower bound of the last place's score, and close:
-  // a few steps up, from one score to the next, reach it.
+  // The need-th of them is a lower bound of the last place's score, and close
+  // while places are few beside lanes: a few steps up, from one score to the
+  // next, reach it.  Steps / bisection, us for 16,384 queries, 5 / 1, 8 key heads:
+  // 512 blocks: 5 places 373 / 416, 13 457 / 463, 17 526 / 481, 29 623 / 508; 1,500
+  // blocks: 5 places 1,259 / 1,449, 11 1,560 / 1,575, 13 1,740 / 1,611, 29 2,315 / 1,837.
+  constexpr int FEW = VPL <= 16 ? 13 : 11;
   float t = __shfl_sync(all, best, min(need, 32) - 1);
   bool found = false;
-  if (need <= 32 && t > -INFINITY)
+  if (need <= FEW && t > -INFINITY)
     for (int round = 0; round < 8; ++round) {
       float c0 = 0.f, c1 = 0.f, next = INFINITY;
 #pragma unroll
