@@ -2,11 +2,13 @@
 // blocks (svg_block_attn) and its gradient (svg_block_attn_backward).
 //
 // The G = Hq/Hk query heads of a key head share the query's list, so the heads
-// of floor(16/G) neighbouring tokens form the 16 rows of a warp's matrix tile.
-// A CTA marks its tokens' blocks in shared bit sets, walks over their union in
-// ascending order, 64 keys at a time, and each row takes part in the blocks
-// that its own token lists: others leave its maximum, sum and accumulator as
-// they were (also where such a block holds infinities or NaN).
+// of neighbouring tokens form the rows of a matrix tile: floor(16/G) tokens with
+// few queries (16-row tiles, here), floor(128/G) with many (tcgen05, in
+// blockattn_tc.cuh).  A CTA marks its tokens' blocks in shared bit sets and walks
+// over their union in ascending order; each row takes part in the blocks that
+// its own token lists: others leave its maximum, sum and accumulator as they
+// were (also where such a block holds infinities or NaN).  Here are the marking,
+// the few-query kernel, and the gradient's work items and joins.
 //
 //   S = scale Q K^T over the visible keys;  m, l: running maximum and sum
 //   O = sum exp(S - m) V / l;  lse = m + log l;  no visible key: O = 0, lse = -inf

@@ -125,7 +125,7 @@ __device__ __forceinline__ bool tc_warp_wait(uint64_t *bar, uint32_t parity, uin
   return __all_sync(0xffffffffu, ok);
 }
 
-// Shared memory of the two query-major kernels: `operands` 128-row tiles, two
+// Shared memory of the forward kernel: `operands` 128-row tiles, two
 // stages of K and V, barriers, bit sets, block list.
 template <int D>
 __host__ __device__ constexpr size_t tc_smem(int operands, int tokens, int nblk) {

@@ -510,12 +510,12 @@ __device__ __noinline__ void select_row_any(const SelectArgs &a, const float *s,
 // head-wise absolute sum and of the block's mean).  The queries' parts stay in
 // registers, the means' stream through two buffers, and the scores go to
 // scratch rows.  A second kernel with a warp per row picks; it needs few
-// registers, so more warps hide its latencies (one kernel for both: 1,570 us
-// against 1,340).  Both run over parts of the queries that bound the scratch.
+// registers, so more warps hide its latencies (one kernel for both took
+// 1.17 times as long).  Both run over parts of the queries that bound the scratch.
 // 32,760 queries, 5 heads to a key head, 8 x 512 blocks: scores 330 us, picking
-// 400 us.  tcgen05 would have twice the rate for these products, but needs 128
-// rows of summed queries a CTA, whose head sums then fill the time (174 us where
-// this takes 143).
+// 400 us.  tcgen05 has twice the rate for these products; a kernel that formed
+// the head sums of 128 rows in each CTA, as this one does of 64, took 174 us a
+// part where this takes 143 (sums formed once beforehand were not tried).
 constexpr int kSelTile = 64, kSelThreads = 128;
 constexpr float kSelSplitError = 1.f / 16384.f;
 

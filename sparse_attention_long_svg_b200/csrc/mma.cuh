@@ -1,7 +1,6 @@
-// Warp-level matrix instructions and asynchronous copies of the kernels whose
-// rows are chosen token by token.  A 16-row tile (mma.sync m16n8k16) holds the
-// query heads of a few tokens; the 128-row tcgen05 tile would need the union of
-// the blocks of 8 times as many tokens, each computed for all of them.
+// Warp-level matrix instructions and asynchronous copies: for attention of few
+// queries, whose 16 rows (mma.sync m16n8k16) would fill an eighth of a 128-row
+// tcgen05 tile, and for the scores of the block choice.
 #pragma once
 
 #include "common.cuh"

@@ -39,7 +39,7 @@ struct RopeArgs {
   float eps;
 };
 
-constexpr int kRopeThreads = 128;       // 335 us for the 480p, 5 s layer (256: 341 us)
+constexpr int kRopeThreads = 128;       // 256: 6 us more of 338 (32,760 tokens x 40 heads, D = 128)
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
   const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kRopeThreads) qk_norm_rope_kernel(const RopeAr
       if (store && h < h1) {
         __nv_bfloat16 *yr = y + h * p.cap[t] * D;
         const uint4 ya = ok ? va[u] : make_uint4(0, 0, 0, 0), yb = ok ? vb[u] : make_uint4(0, 0, 0, 0);
-        if (U > 1) {                   // far more than L2 holds: do not keep it there (340 against 355 us)
+        if (U > 1) {                   // a large call: streaming, 15 us less of 338
           __stcs(reinterpret_cast<uint4 *>(yr), ya);
           __stcs(reinterpret_cast<uint4 *>(yr + D / 2), yb);
         } else {

@@ -1025,9 +1025,10 @@ svg_status block_shapes(int BHq, int BHk, int B, int Nq, int Nk, int D, int bloc
 bool select_few(int BHk, int Nq) { return Nq <= 4 || (Nq <= 32 && static_cast<int64_t>(BHk) * Nq <= 512); }
 int64_t select_items(int BHk, int Nq) { return static_cast<int64_t>(BHk) * ((Nq + kSelTile - 1) / kSelTile); }
 // Items of a part: a multiple of what runs at a time (3 per SM) whose scores take
-// at most 256 MiB.  32,760 queries x 8 key heads x 512 blocks: 64 MiB, which
-// stay in L2, 883 us; 128 MiB 816 us; 256 MiB 768 us (fewer launches with a
-// tail each).
+// at most 256 MiB, or one such wave where that takes more (beyond 2,360 blocks:
+// up to 465 MB at 4,096).  32,760 queries x 8 key heads x 512 blocks take 1.15
+// times as long with parts of 64 MiB, which stay in L2, and 1.06 times with 128
+// MiB: fewer launches with a tail each count for more.
 constexpr int64_t kSelPartBytes = 256ll << 20;
 int64_t select_part(int BHk, int Nq, int nblk) {
   const int64_t row = (nblk + kSelTile - 1) / kSelTile * kSelTile * sizeof(float);
@@ -1077,6 +1078,10 @@ struct BlockAttnPlan {
   bool few;
   int tokens, tiles, splits;
 };
+// Few queries, one 16-row tile: the few-query kernel; more: 128-row tiles.  us,
+// few-query / many-query kernel, 32 blocks: one sequence x 8 heads, G = 1, 4
+// queries 30 / 42, 32 queries 44 / 58; 16 sequences, G = 5: 1 query 41 / 46, 4
+// queries (two 16-row tiles) 88 / 64, 32 queries 455 / 236.
 // Few CTAs: the union of a tile's blocks is split into what one wave of CTAs
 // holds, at least 4 x 64 keys to a part.
 BlockAttnPlan block_attn_plan(int BHq, int BHk, int Nq, int nblk, int topk, int block) {
@@ -1348,8 +1353,11 @@ svg_status svg_block_attn_backward(const void *dout, const void *q, const void *
     return D == 128 ? tc_dq_smem<128>(stages, t, nblk) : tc_dq_smem<64>(stages, t, nblk);
   };
   const int tokens = tile_tokens(BHq / BHk);
-  // A second stage of K where two CTAs still share an SM (D = 128: lists of up
-  // to a few hundred blocks).
+  // A second stage of K where two CTAs still share an SM (D = 128, G = 5: up to
+  // 160 blocks).  us, two stages / one: 8,190 tokens, G = 5, 1,738 / 2,002; D = 64,
+  // G = 1, 6,000 tokens, 460 / 536.  Where it would cost the second CTA, long lists
+  // lose (G = 1, 20,000 tokens: 2,583 / 2,310) and short ones gain a little (8,190
+  // tokens: 435 / 474).
   const int k_stages = dq_bytes(2, tokens) <= kHalfSmem ? 2 : 1;
   const int64_t ctas = static_cast<int64_t>(BHk) * ((Nq + tokens - 1) / tokens);
   if (tiles >= (1ll << 31) - 1 || w.max_items >= (1ll << 31) - 1 || (listed + 255) / 256 >= (1ll << 31) ||
